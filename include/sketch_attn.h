@@ -201,6 +201,33 @@ sa_status sa_forward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* o
                                float* S, float* mass, float* H, void* S_bf16, void* workspace,
                                size_t ws_bytes, sa_stream_t stream);
 
+size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_dtype x_dtype);
+
+/*
+ * sa_backward_tokenwise -- gradients of L = sum_u <dS_u, S_u> through
+ * sa_forward_tokenwise (the paper trains its baselines end to end and prints no
+ * backward; these are the chain-rule derivatives).  The probabilities are
+ * recomputed from X.  With U = P W_Q W_K^T / sqrt(d), i_u = 1/(m_u + eps) (m = 1
+ * for a user with events, 0 without) and A the forward's token-wise softmax:
+ *   dW_V = sum_u i_u H^T dS;  dH = i_u dS W_V^T;  c_j = dH_j . H_j
+ *   dZ = A o (dH X_u^T - c);  dX = A^T dH + dZ^T U;  E = sum_u dZ X_u
+ *   dP = E W_K W_Q^T/sqrt(d);  dW_Q = P^T E W_K/sqrt(d);  dW_K = E^T P W_Q/sqrt(d)
+ * The mass is constant, so it has no gradient.
+ * Inputs as sa_forward_tokenwise, plus its H [B,k,d] (zero rows for a user
+ * without events, as that call writes them) and dS [B,k,d] fp32.
+ * dX [n_total, d] bf16 out (must not be X); dP [k,d], dW_Q, dW_K, dW_V [d,d] fp32
+ * out (sums over the batch).  bf16 X and d = 128 only (else SA_ERR_UNSUPPORTED),
+ * 1 <= k <= 4096.  The weight gradients hold fp32-grade accuracy (about 1e-6
+ * relative); the same inputs give the same bits.  Workspace:
+ * sa_backward_tokenwise_workspace bytes, caller owned.  Asynchronous on stream.
+ */
+sa_status sa_backward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* offsets_host,
+                                const int64_t* offsets_dev, int B, int k, int d, const float* P,
+                                const float* W_Q, const float* W_K, const float* W_V, float eps,
+                                const float* H, const float* dS, void* dX, float* dP, float* dW_Q,
+                                float* dW_K, float* dW_V, void* workspace, size_t ws_bytes,
+                                sa_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* Stacked refinement                                                        */
 /* ------------------------------------------------------------------------ */
@@ -298,6 +325,27 @@ sa_status sa_refine_backward(const void* X, sa_dtype x_dtype, const int64_t* off
 sa_status sa_gather_events(const void* item_table, int64_t vocab, const void* action_table,
                            int n_actions, const int32_t* item_ids, const uint8_t* action_ids,
                            int64_t n, int d, void* X, sa_stream_t stream);
+
+size_t sa_gather_events_backward_workspace(int64_t n, int64_t vocab, int n_actions, int d);
+
+/*
+ * sa_gather_events_backward -- the gradients of both tables through
+ * sa_gather_events: given dX [n, d] (SA_BF16, as sa_backward writes it, or SA_F32,
+ * as sa_refine_backward does),
+ *   d_item_table[v]   = sum over {i : item_ids[i] = v} of dX[i]     [vocab, d]
+ *   d_action_table[a] = sum over {i : action_ids[i] = a} of dX[i]   [n_actions, d]
+ * fp32, dense (rows that no event names are zeros), overwritten; either output may
+ * be NULL and is then not computed.  Sums are fp32 in a fixed order: the same
+ * inputs give the same bits.  An event whose id or action is outside its table had
+ * a zero row in the forward: it counts for neither output and makes the next
+ * sa_poll_device_status return SA_ERR_INVALID_ARG.
+ * d a multiple of 8, n_actions <= 256, n and vocab < 2^31.  Workspace:
+ * sa_gather_events_backward_workspace bytes, 16-byte aligned, caller owned.
+ */
+sa_status sa_gather_events_backward(const int32_t* item_ids, const uint8_t* action_ids, int64_t n,
+                                    const void* dX, sa_dtype dx_dtype, int64_t vocab, int n_actions,
+                                    int d, float* d_item_table, float* d_action_table,
+                                    void* workspace, size_t ws_bytes, sa_stream_t stream);
 
 size_t sa_gather_events_fused_workspace(int n_actions, int d, int d_ff);
 
@@ -467,6 +515,63 @@ sa_status stca_backward_full(const void* q, sa_dtype dtype,
  */
 sa_status stca_fuse(const float* z_r, const float* z_u, const float* W_F, const float* b_F,
                     int64_t C, int D, float* out, sa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Optimiser                                                                 */
+/* ------------------------------------------------------------------------ */
+/* How a tensor's two moments are held. */
+typedef enum {
+  SA_STATE_F32 = 0,   /* m, v: fp32 [n] */
+  SA_STATE_8BIT = 1   /* m, v: e4m3 [n] and one fp32 scale per 128 values: the first moment is
+                         m_scale[i / 128] * m[i], the second (v_scale[i / 128] * v[i])^2 */
+} sa_state_kind;
+
+/* One parameter tensor of an AdamW step (device pointers, flat arrays of n values). */
+typedef struct {
+  float* param;            /* [n] fp32, updated */
+  const void* grad;        /* [n] grad_dtype */
+  sa_dtype grad_dtype;
+  sa_state_kind state;
+  void* m;                 /* [n] first moment, updated */
+  void* v;                 /* [n] second moment (8-bit: its square root), updated */
+  float* m_scale;          /* [ceil(n / 128)], updated; 8-bit states only (else NULL) */
+  float* v_scale;          /* [ceil(n / 128)], updated; 8-bit states only (else NULL) */
+  void* param_bf16;        /* [n] bf16 out: the updated param rounded, or NULL */
+  int64_t n;
+  float weight_decay;      /* decoupled; 0 for none */
+} sa_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;                 /* t >= 1 of this step (unless step_dev) */
+  /* Optional device scalars, read when the kernel runs, so that a captured step can be
+   * replayed with new values: t, lr, and a factor on every gradient (a clipping
+   * coefficient or the inverse of a loss scale).  NULL: step, lr, 1.  A grad_scale that
+   * is not finite leaves every tensor as it is. */
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale_dev;
+} sa_adamw_config;
+
+/*
+ * sa_adamw_step -- one AdamW step over n_tensors tensors (no counterpart in the
+ * paper, which does not name its optimiser).  Per value, in fp32, with
+ * g = grad * grad_scale and t the step:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   param = param (1 - lr weight_decay)
+ *           - lr/(1 - beta1^t) * m / (sqrt(v)/sqrt(1 - beta2^t) + eps)
+ * 8-bit states are rounded after the update has used them: per 128 values scale =
+ * (largest magnitude)/448, codes = value/scale to nearest even; a positive sqrt(v) rounds to the
+ * smallest positive code (2^-9) rather than to zero.  A block whose largest
+ * magnitude is below 2^-100 is held as zeros; a gradient that is not finite makes
+ * the moments of its block of 128 NaN.  All-zero codes and scales are the fresh state.
+ * The tensors must not overlap; param, grad, m, v and param_bf16 are 16-byte aligned,
+ * the scales 4-byte aligned.  The list is read during
+ * the call only; one kernel is launched per 192 tensors.  A tensor with n = 0 is
+ * skipped.  0 <= beta1, beta2 < 1, eps >= 0, lr and weight_decay finite.
+ */
+sa_status sa_adamw_step(const sa_adamw_tensor* tensors, int n_tensors, const sa_adamw_config* config,
+                        sa_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Measurement support (not part of the method)                              */

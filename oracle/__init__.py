@@ -56,6 +56,7 @@ __all__ = [
     "sa_forward", "sa_user", "sa_backward", "stca_branch", "stca_branch_reordered",
     "stca_fuse", "assignment", "token_lse", "layer_norm", "swiglu_ffn", "sa_refine_user",
     "sa_refine", "tokenwise_user", "sa_forward_tokenwise", "stca_branch_grads", "event_rows",
+    "sa_backward_tokenwise", "event_table_grads", "adamw_step",
 ]
 
 
@@ -507,3 +508,54 @@ def sa_forward_tokenwise(X, offsets: Sequence[int], P, W_Q, W_K, W_V, eps: float
     for u in range(B):
         S[u], mass[u], H[u] = tokenwise_user(X[offsets[u]:offsets[u + 1]], P, W_Q, W_K, W_V, eps)
     return S, mass, H
+
+
+def sa_backward_tokenwise(X, offsets: Sequence[int], P, W_Q, W_K, W_V, eps: float, dS, H=None):
+    """Gradients of <dS, S> through sa_forward_tokenwise: (dX, dP, dW_Q, dW_K, dW_V).  With
+    i = 1/(m + eps) (m = 1 for a user with events) and U = P W_Q W_K^T / sqrt(d):
+        dW_V = sum_u i H^T dS,  dH = i dS W_V^T,  dZ = A o (dH X^T - rowsum(dH o H)),
+        dX = A^T dH + dZ^T U,  E = sum_u dZ X,
+        dP = E W_K W_Q^T / sqrt(d),  dW_Q = P^T E W_K / sqrt(d),  dW_K = E^T P W_Q / sqrt(d).
+    H: the forward's A X, if the caller holds one (else computed here).  A user with one event
+    has a constant softmax: its dZ is zero."""
+    X, P, W_Q, W_K, W_V, dS = (_f64(a) for a in (X, P, W_Q, W_K, W_V, dS))
+    root = math.sqrt(P.shape[1])
+    U = P @ W_Q @ W_K.T / root
+    dX, E, dWV = np.zeros_like(X), np.zeros_like(P), np.zeros_like(W_V)
+    for u in range(len(offsets) - 1):
+        lo, hi = int(offsets[u]), int(offsets[u + 1])
+        if lo == hi:
+            continue
+        x = X[lo:hi]
+        A = _softmax_rows(U @ x.T)
+        h = A @ x if H is None else _f64(H[u])
+        dWV += h.T @ dS[u] / (1.0 + eps)
+        dH = dS[u] @ W_V.T / (1.0 + eps)
+        dZ = A * (dH @ x.T - (dH * h).sum(axis=1, keepdims=True)) if hi - lo > 1 else np.zeros_like(A)
+        dX[lo:hi] = A.T @ dH + dZ.T @ U
+        E += dZ @ x
+    return dX, E @ W_K @ W_Q.T / root, P.T @ E @ W_K / root, E.T @ P @ W_Q / root, dWV
+
+
+# --------------------------------------------------------------------------
+# Training: the event tables' gradients and the AdamW step
+# --------------------------------------------------------------------------
+def event_table_grads(item_ids, action_ids, dX, vocab: int, n_actions: int):
+    """(d_item [vocab, d], d_action [n_actions, d]) through event_rows; an event whose id or
+    action is outside its table counts for neither."""
+    dX = _f64(dX)
+    ids, acts = np.asarray(item_ids, np.int64), np.asarray(action_ids, np.int64)
+    ok = (ids >= 0) & (ids < vocab) & (acts < n_actions)
+    item, action = np.zeros((vocab, dX.shape[1])), np.zeros((n_actions, dX.shape[1]))
+    np.add.at(item, ids[ok], dX[ok])
+    np.add.at(action, acts[ok], dX[ok])
+    return item, action
+
+
+def adamw_step(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step: int, grad_scale: float = 1.0):
+    """One AdamW step with decoupled weight decay: the new (p, m, v)."""
+    p, g, m, v = _f64(p), _f64(g) * grad_scale, _f64(m), _f64(v)
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    hat_m, hat_v = m / (1 - beta1 ** step), v / (1 - beta2 ** step)
+    return p - lr * (weight_decay * p + hat_m / (np.sqrt(hat_v) + eps)), m, v

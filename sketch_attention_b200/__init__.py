@@ -10,6 +10,7 @@ Entry points keep the C names: ``sa_forward``, ``sa_backward``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -33,7 +34,9 @@ EXPORTS = ("sa_version", "sa_last_error", "sa_poll_device_status", "sa_forward_w
            "stca_forward_full_workspace", "stca_forward_full", "stca_backward_full_workspace",
            "stca_backward_full", "sa_gather_events", "sa_gather_events_fused",
            "sa_gather_events_fused_workspace", "sa_measure_exp2_rate", "sa_selftest_bounded_wait",
-           "sa_refine_backward_workspace", "sa_refine_backward")
+           "sa_refine_backward_workspace", "sa_refine_backward", "sa_backward_tokenwise_workspace",
+           "sa_backward_tokenwise", "sa_gather_events_backward_workspace", "sa_gather_events_backward",
+           "sa_adamw_step")
 
 
 class SAError(RuntimeError):
@@ -71,6 +74,23 @@ REFINE_GRAD_KEYS = ("dW_Q", "dW_K", "dln1_g", "dln1_b", "dW1", "dW3", "dW2", "dl
 
 class RefineLayerGradC(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in REFINE_GRAD_KEYS]
+
+
+SA_STATE_F32, SA_STATE_8BIT = 0, 1
+ADAMW_BLOCK = 128        # values per scale of an 8-bit state
+
+
+class AdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("grad_dtype", ctypes.c_int),
+                ("state", ctypes.c_int), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float)]
+
+
+class AdamWConfigC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -150,6 +170,17 @@ def load(path: Optional[str] = None):
     lib.sa_refine_backward.restype = _i
     lib.sa_refine_backward.argtypes = [_vp, _i, _vp, _vp, _i, _i, _i, _vp, _i, ctypes.POINTER(RefineLayerC), _f,
                                        _vp, _vp, _vp, ctypes.POINTER(RefineLayerGradC), _vp, _sz, _vp]
+    lib.sa_backward_tokenwise_workspace.restype = _sz
+    lib.sa_backward_tokenwise_workspace.argtypes = [_i, _i64, _i, _i, _i]
+    lib.sa_backward_tokenwise.restype = _i
+    lib.sa_backward_tokenwise.argtypes = [_vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _f, _vp, _vp,
+                                          _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.sa_gather_events_backward_workspace.restype = _sz
+    lib.sa_gather_events_backward_workspace.argtypes = [_i64, _i64, _i, _i]
+    lib.sa_gather_events_backward.restype = _i
+    lib.sa_gather_events_backward.argtypes = [_vp, _vp, _i64, _vp, _i, _i64, _i, _i, _vp, _vp, _vp, _sz, _vp]
+    lib.sa_adamw_step.restype = _i
+    lib.sa_adamw_step.argtypes = [ctypes.POINTER(AdamWTensorC), _i, ctypes.POINTER(AdamWConfigC), _vp]
     lib.sa_launch_count.restype = ctypes.c_longlong
     lib.sa_profile.restype = _i
     lib.sa_profile.argtypes = [_i]
@@ -202,6 +233,29 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _need(name: str, t: torch.Tensor, dtype, shape, device):
+    """t is a contiguous CUDA tensor of that dtype, shape and device."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t
+
+
+def _at(device, stream):
+    """Runs a call on its tensors' device and on `stream`: buffers allocated inside belong to that
+    stream, so the allocator hands them out again only behind the call's kernels."""
+    if stream is None:
+        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 # --------------------------------------------------------------------------
@@ -283,6 +337,44 @@ def sa_forward_tokenwise(X: torch.Tensor, offsets, P, W_Q, W_K, W_V, eps: float 
         res["H"] = H
     if Sb is not None:
         res["S_bf16"] = Sb
+    return res
+
+
+def sa_backward_tokenwise_workspace(B: int, n_total: int, k: int, d: int, x_dtype: int) -> int:
+    return int(load().sa_backward_tokenwise_workspace(B, n_total, k, d, x_dtype))
+
+
+def sa_backward_tokenwise(X: torch.Tensor, offsets, P, W_Q, W_K, W_V, eps: float, H, dS, *,
+                          offsets_dev: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Gradients {"dX", "dP", "dW_Q", "dW_K", "dW_V"} of <dS, S> through sa_forward_tokenwise,
+    given its H; dX is bf16, the others fp32.  ``out`` may supply any of these buffers."""
+    lib = load()
+    off = _host_i64(offsets)
+    B, n = len(off) - 1, int(off[-1])
+    k, d = P.shape
+    dev, f32 = X.device, torch.float32
+    _need("X", X, torch.bfloat16, (n, d), dev)
+    for name, t, shape in (("P", P, (k, d)), ("W_Q", W_Q, (d, d)), ("W_K", W_K, (d, d)), ("W_V", W_V, (d, d)),
+                           ("H", H, (B, k, d)), ("dS", dS, (B, k, d))):
+        _need(name, t, f32, shape, dev)
+    if offsets_dev is not None:
+        _need("offsets_dev", offsets_dev, torch.int64, (B + 1,), dev)
+    with _at(dev, stream):
+        res = {}
+        for name, dt, shape in (("dX", torch.bfloat16, (n, d)), ("dP", f32, (k, d)), ("dW_Q", f32, (d, d)),
+                                ("dW_K", f32, (d, d)), ("dW_V", f32, (d, d))):
+            t = out.get(name) if out else None
+            res[name] = torch.empty(shape, dtype=dt, device=dev) if t is None else _need(name, t, dt, shape, dev)
+        ws_bytes = lib.sa_backward_tokenwise_workspace(B, n, k, d, SA_BF16)
+        if workspace is None or workspace.numel() < ws_bytes:
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        offd = _dev_i64(off, dev, offsets_dev)
+        st = lib.sa_backward_tokenwise(_p(X), SA_BF16, _hp(off), _p(offd), B, k, d, _p(P), _p(W_Q), _p(W_K), _p(W_V),
+                                       float(eps), _p(H), _p(dS), _p(res["dX"]), _p(res["dP"]), _p(res["dW_Q"]),
+                                       _p(res["dW_K"]), _p(res["dW_V"]), _p(workspace), workspace.numel(),
+                                       _stream(stream))
+        _check("sa_backward_tokenwise", st)
     return res
 
 
@@ -468,6 +560,89 @@ def sa_gather_events(item_table: torch.Tensor, action_table: torch.Tensor, item_
                               _p(item_ids), _p(action_ids), n, d, _p(X), _stream(stream))
     _check("sa_gather_events", st)
     return X
+
+
+def sa_gather_events_backward_workspace(n: int, vocab: int, n_actions: int, d: int) -> int:
+    return int(load().sa_gather_events_backward_workspace(n, vocab, n_actions, d))
+
+
+def sa_gather_events_backward(item_ids: torch.Tensor, action_ids: torch.Tensor, dX: torch.Tensor, vocab: int,
+                              n_actions: int, *, want_item: bool = True, want_action: bool = True,
+                              out: Optional[dict] = None, workspace: Optional[torch.Tensor] = None,
+                              stream=None) -> dict:
+    """The tables' gradients through sa_gather_events: {"d_item": [vocab, d], "d_action": [n_actions, d]},
+    fp32, from dX [n, d] (bf16 or fp32).  ``out`` may supply the buffers."""
+    lib = load()
+    n, d = dX.shape
+    dev = dX.device
+    _need("dX", dX, dX.dtype, (n, d), dev)
+    _need("item_ids", item_ids, torch.int32, (n,), dev)
+    _need("action_ids", action_ids, torch.uint8, (n,), dev)
+    with _at(dev, stream):
+        res = {}
+        for name, want, rows in (("d_item", want_item, vocab), ("d_action", want_action, n_actions)):
+            t = out.get(name) if out else None
+            if t is not None:
+                res[name] = _need(name, t, torch.float32, (rows, d), dev)
+            elif want:
+                res[name] = torch.empty(rows, d, device=dev)
+        ws_bytes = lib.sa_gather_events_backward_workspace(n, vocab, n_actions, d)
+        if workspace is None or workspace.numel() < ws_bytes:
+            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+        st = lib.sa_gather_events_backward(_p(item_ids), _p(action_ids), n, _p(dX), _dtype_code(dX), vocab, n_actions,
+                                           d, _p(res.get("d_item")), _p(res.get("d_action")), _p(workspace),
+                                           workspace.numel(), _stream(stream))
+        _check("sa_gather_events_backward", st)
+    return res
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step, described once for many steps.  ``tensors``: dicts with
+    "param" (fp32), "grad" (fp32 or bf16), "m" and "v" (both fp32, or both float8_e4m3fn with
+    "m_scale" and "v_scale", fp32, one value per ADAMW_BLOCK values), all of one size and device;
+    optionally "param_bf16" (bf16, receives the rounded parameter) and "weight_decay" (default 0).
+    The arrays are held by reference: a step reads and updates them in place."""
+
+    def __init__(self, tensors: Sequence[dict]):
+        self.tensors = [dict(t) for t in tensors]
+        self.c = (AdamWTensorC * max(len(self.tensors), 1))()
+        self.device = self.tensors[0]["param"].device if self.tensors else None
+        for c, t in zip(self.c, self.tensors):
+            n = t["param"].numel()
+            flat = lambda name: t[name].view(-1) if t[name].is_contiguous() else t[name]  # noqa: E731
+            need = lambda name, dt, size=n: _need(name, flat(name), dt, (size,), self.device).data_ptr()  # noqa: E731
+            c.n, c.weight_decay = n, float(t.get("weight_decay", 0.0))
+            c.param = need("param", torch.float32)
+            c.grad, c.grad_dtype = need("grad", t["grad"].dtype), _dtype_code(t["grad"])
+            if t["m"].dtype == torch.float8_e4m3fn:
+                blocks = -(-n // ADAMW_BLOCK)
+                c.state, c.m, c.v = SA_STATE_8BIT, need("m", torch.float8_e4m3fn), need("v", torch.float8_e4m3fn)
+                c.m_scale, c.v_scale = need("m_scale", torch.float32, blocks), need("v_scale", torch.float32, blocks)
+            else:
+                c.state, c.m, c.v = SA_STATE_F32, need("m", torch.float32), need("v", torch.float32)
+            if t.get("param_bf16") is not None:
+                c.param_bf16 = need("param_bf16", torch.bfloat16)
+
+
+def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, *, step: int = 0,
+                  step_dev: Optional[torch.Tensor] = None, lr_dev: Optional[torch.Tensor] = None,
+                  grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One AdamW step, in place, over an AdamWTensors (or a list of its dicts).  ``step`` counts from
+    1; ``step_dev`` (int64), ``lr_dev`` and ``grad_scale`` (fp32) are optional one-value CUDA tensors
+    read when the step runs (for captured steps, clipping and loss scaling)."""
+    lib = load()
+    if not isinstance(tensors, AdamWTensors):
+        tensors = AdamWTensors(tensors)
+    if tensors.device is None:
+        return
+    dev = tensors.device
+    for name, t, dt in (("step_dev", step_dev, torch.int64), ("lr_dev", lr_dev, torch.float32),
+                        ("grad_scale", grad_scale, torch.float32)):
+        if t is not None:
+            _need(name, t.view(-1), dt, (1,), dev)
+    cfg = AdamWConfigC(lr, beta1, beta2, eps, step, _p(step_dev), _p(lr_dev), _p(grad_scale))
+    with _at(dev, stream):
+        _check("sa_adamw_step", lib.sa_adamw_step(tensors.c, len(tensors.tensors), ctypes.byref(cfg), _stream(stream)))
 
 
 def sa_gather_events_fused_workspace(n_actions: int, d: int = 128, d_ff: int = 256) -> int:

@@ -11,8 +11,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsketchattn.so")
-SOURCES = ["api.cu", "gemm.cu", "sa_simt.cu", "sa_tc.cu", "sa_bwd_tc.cu", "sa_refine.cu", "sa_refine_bwd.cu", "sa_tokenwise.cu", "sa_noalloc.cu", "stca.cu",
-           "stca_tc.cu", "stca_full.cu", "stca_ffn_tc.cu", "stca_bwd.cu", "events.cu", "measure.cu", "tc_gemm.cu"]
+SOURCES = ["api.cu", "gemm.cu", "sa_simt.cu", "sa_tc.cu", "sa_bwd_tc.cu", "sa_refine.cu", "sa_refine_bwd.cu", "sa_tokenwise.cu", "sa_tokenwise_bwd.cu", "sa_noalloc.cu", "stca.cu",
+           "stca_tc.cu", "stca_full.cu", "stca_ffn_tc.cu", "stca_bwd.cu", "events.cu", "events_bwd.cu", "adamw.cu", "measure.cu", "tc_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -2,6 +2,7 @@
 // and dispatch to the kernels.  Host-side only; no allocation anywhere.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -386,6 +387,50 @@ sa_status sa_forward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* o
   return sa_tokenwise_run(a, w, (cudaStream_t)stream);
 }
 
+size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_dtype x_dtype) {
+  if (B < 1 || k < 1 || k > 4096 || n_total < 0 || x_dtype != SA_BF16 || d != 128) return 0;
+  return tokenwise_bwd_layout(nullptr, B, n_total, k, d, nullptr);
+}
+
+sa_status sa_backward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* offsets_host,
+                                const int64_t* offsets_dev, int B, int k, int d, const float* P,
+                                const float* W_Q, const float* W_K, const float* W_V, float eps,
+                                const float* H, const float* dS, void* dX, float* dP, float* dW_Q,
+                                float* dW_K, float* dW_V, void* workspace, size_t ws_bytes,
+                                sa_stream_t stream) {
+  SA_TRY(check_sa_shape(B, k, d, x_dtype));
+  if (x_dtype != SA_BF16 || d != 128)
+    return fail(SA_ERR_UNSUPPORTED, "sa_backward_tokenwise needs bf16 X and d = 128");
+  SA_TRY(check_offsets(offsets_host, B, "offsets_host"));
+  const int64_t n = offsets_host[B];
+  if (n >= (1LL << 31) - 256 || (int64_t)B * ((k + 127) / 128 * 128) >= (1LL << 31))
+    return fail(SA_ERR_UNSUPPORTED, "n_total and B * k must be < 2^31 (k rounded up to a multiple of 128)");
+  if (!(eps >= 0.f)) return fail(SA_ERR_INVALID_ARG, "eps must be >= 0");
+  SA_TRY(check_ptr(X, "X", n == 0));
+  SA_TRY(check_ptr(offsets_dev, "offsets_dev"));
+  SA_TRY(check_ptr(P, "P"));
+  SA_TRY(check_ptr(W_Q, "W_Q"));
+  SA_TRY(check_ptr(W_K, "W_K"));
+  SA_TRY(check_ptr(W_V, "W_V"));
+  SA_TRY(check_ptr(H, "H"));
+  SA_TRY(check_ptr(dS, "dS"));
+  SA_TRY(check_ptr(dX, "dX", n == 0));
+  SA_TRY(check_ptr(dP, "dP"));
+  SA_TRY(check_ptr(dW_Q, "dW_Q"));
+  SA_TRY(check_ptr(dW_K, "dW_K"));
+  SA_TRY(check_ptr(dW_V, "dW_V"));
+  if (dX && dX == X) return fail(SA_ERR_INVALID_ARG, "dX must not alias X");
+  const size_t need = tokenwise_bwd_layout(nullptr, B, n, k, d, nullptr);
+  if (!workspace || ws_bytes < need)
+    return fail(SA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  SA_TRY(check_ptr(workspace, "workspace"));
+  TokenwiseBwdWork w;
+  tokenwise_bwd_layout(workspace, B, n, k, d, &w);
+  SaBwdArgs a{X, x_dtype, offsets_dev, B, n, k, d, P, W_Q, W_K, W_V, eps, H, nullptr, dS, nullptr, nullptr,
+              dX, dP, dW_Q, dW_K, dW_V};
+  return sa_tokenwise_backward_run(a, w, (cudaStream_t)stream);
+}
+
 size_t sa_refine_workspace(int B, int64_t n_total, int k, int d, sa_dtype x_dtype) {
   if (B < 1 || k < 1 || d < 1 || n_total < 0 || !sa_tc_supported(x_dtype, k, d)) return 0;
   return refine_layout(nullptr, B, n_total, k, d, nullptr, nullptr);
@@ -736,6 +781,67 @@ sa_status sa_gather_events(const void* item_table, int64_t vocab, const void* ac
   SA_TRY(check_ptr(X, "X", n == 0));
   return gather_events_run(item_table, vocab, action_table, n_actions, item_ids, action_ids, n, d, X,
                            (cudaStream_t)stream);
+}
+
+size_t sa_gather_events_backward_workspace(int64_t n, int64_t vocab, int n_actions, int d) {
+  if (n < 0 || n >= (1LL << 31) || vocab < 1 || vocab >= (1LL << 31) || n_actions < 1 || n_actions > 256 || d < 8 ||
+      d % 8 != 0)
+    return 0;
+  return events_bwd_layout(nullptr, n, vocab, n_actions, d, nullptr);
+}
+
+sa_status sa_gather_events_backward(const int32_t* item_ids, const uint8_t* action_ids, int64_t n, const void* dX,
+                                    sa_dtype dx_dtype, int64_t vocab, int n_actions, int d, float* d_item_table,
+                                    float* d_action_table, void* workspace, size_t ws_bytes, sa_stream_t stream) {
+  if (n < 0 || vocab < 1 || n_actions < 1 || n_actions > 256) return fail(SA_ERR_INVALID_ARG, "bad sizes");
+  if (dx_dtype != SA_F32 && dx_dtype != SA_BF16) return fail(SA_ERR_INVALID_ARG, "bad dtype");
+  if (d < 8 || d % 8 != 0) return fail(SA_ERR_UNSUPPORTED, "d must be a positive multiple of 8");
+  if (n >= (1LL << 31) || vocab >= (1LL << 31)) return fail(SA_ERR_UNSUPPORTED, "n and vocab must be < 2^31");
+  // the ids are read element by element: any alignment of their type will do
+  if (n > 0 && (!item_ids || !action_ids)) return fail(SA_ERR_INVALID_ARG, "item_ids or action_ids is NULL");
+  if (((uintptr_t)item_ids & 3) != 0) return fail(SA_ERR_INVALID_ARG, "item_ids is not 4-byte aligned");
+  SA_TRY(check_ptr(dX, "dX", n == 0));
+  SA_TRY(check_ptr(d_item_table, "d_item_table", true));
+  SA_TRY(check_ptr(d_action_table, "d_action_table", true));
+  const size_t need = events_bwd_layout(nullptr, n, vocab, n_actions, d, nullptr);
+  if (!workspace || ws_bytes < need)
+    return fail(SA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  SA_TRY(check_ptr(workspace, "workspace"));
+  EventsBwdWork w;
+  events_bwd_layout(workspace, n, vocab, n_actions, d, &w);
+  return events_bwd_run(dX, dx_dtype, item_ids, action_ids, n, vocab, n_actions, d, d_item_table, d_action_table, w,
+                        (cudaStream_t)stream);
+}
+
+sa_status sa_adamw_step(const sa_adamw_tensor* tensors, int n_tensors, const sa_adamw_config* config,
+                        sa_stream_t stream) {
+  if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return fail(SA_ERR_INVALID_ARG, "bad tensor list");
+  if (!config) return fail(SA_ERR_INVALID_ARG, "config is NULL");
+  const sa_adamw_config& c = *config;
+  if (!(c.beta1 >= 0.0 && c.beta1 < 1.0) || !(c.beta2 >= 0.0 && c.beta2 < 1.0))
+    return fail(SA_ERR_INVALID_ARG, "beta1 and beta2 must be in [0, 1)");
+  if (!(c.eps >= 0.0) || !std::isfinite(c.eps)) return fail(SA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!c.lr_dev && !std::isfinite(c.lr)) return fail(SA_ERR_INVALID_ARG, "lr must be finite");
+  if (!c.step_dev && c.step < 1) return fail(SA_ERR_INVALID_ARG, "step must be >= 1");
+  if (((uintptr_t)c.step_dev & 7) || ((uintptr_t)c.lr_dev & 3) || ((uintptr_t)c.grad_scale_dev & 3))
+    return fail(SA_ERR_INVALID_ARG, "a device scalar is not aligned to its type");
+  for (int i = 0; i < n_tensors; ++i) {
+    const sa_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return fail(SA_ERR_INVALID_ARG, "tensors[].n must be >= 0");
+    if (t.grad_dtype != SA_F32 && t.grad_dtype != SA_BF16) return fail(SA_ERR_INVALID_ARG, "bad grad_dtype");
+    if (t.state != SA_STATE_F32 && t.state != SA_STATE_8BIT) return fail(SA_ERR_INVALID_ARG, "bad state kind");
+    if (!std::isfinite(t.weight_decay)) return fail(SA_ERR_INVALID_ARG, "weight_decay must be finite");
+    const bool none = t.n == 0, f32 = t.state == SA_STATE_F32;
+    SA_TRY(check_ptr(t.param, "tensors[].param", none));
+    SA_TRY(check_ptr(t.grad, "tensors[].grad", none));
+    SA_TRY(check_ptr(t.m, "tensors[].m", none));
+    SA_TRY(check_ptr(t.v, "tensors[].v", none));
+    // the scales are read one by one: any alignment of their type will do
+    if (!f32 && !none && (!t.m_scale || !t.v_scale || ((uintptr_t)t.m_scale & 3) || ((uintptr_t)t.v_scale & 3)))
+      return fail(SA_ERR_INVALID_ARG, "an 8-bit state needs m_scale and v_scale");
+    SA_TRY(check_ptr(t.param_bf16, "tensors[].param_bf16", true));
+  }
+  return adamw_run(tensors, n_tensors, c, (cudaStream_t)stream);
 }
 
 size_t sa_gather_events_fused_workspace(int n_actions, int d, int d_ff) {

@@ -128,6 +128,40 @@ struct TokenwiseWork {
 size_t tokenwise_layout(void* base, int B, int k, int d, TokenwiseWork* w);
 sa_status sa_tokenwise_run(const SaFwdArgs& a, const TokenwiseWork& w, cudaStream_t st);
 
+// Its backward (sa_tokenwise_bwd.cu).  kp: k rounded up to whole 128-prototype slices.
+struct TokenwiseBwdWork {
+  Chunking chE;          // token chunks of the per-slice kernels (row statistics, E)
+  Chunking chX;          // token chunks of the dX kernel
+  float* T;              // [d, d]
+  float* Pf;             // [k, d] folded prototypes, base-2 units
+  __nv_bfloat16 *Uhi, *Ulo;   // [kp, d] the same as hi + lo
+  __nv_bfloat16 *Hhi, *Hlo;   // [B, kp, d] dH as hi + lo
+  float *c, *c2;         // [B, kp] dH . H, and ln2 times it
+  float* lse2;           // [B, kp] log2 of the rows' sums of 2^z
+  float2* stat_user;     // [B, 2, kp] (max, sum) of users inside one chunk
+  float2* stat_slot;     // [G, 2, 2, kp] of the pieces of users that span chunks
+  float* Epart;          // [G, k, d]
+  float *E, *dQ, *Q;     // [k, d]
+  float* gsplit;         // [kMaxSplit, d, d]
+};
+size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, TokenwiseBwdWork* w);
+sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st);
+
+// Gradients of the event tables (events_bwd.cu).
+struct EventsBwdWork {
+  uint32_t *keys[2], *events[2];   // [n] sorted item ids and their events, in two buffers
+  int* hist;             // [sort CTAs, 1024] digit counts
+  float* pieces;         // [n / 256, d] sums of list pieces that one item fills
+  float* action_part;    // [action CTAs, n_actions, d]
+};
+size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, int d, EventsBwdWork* w);
+sa_status events_bwd_run(const void* dX, sa_dtype dtype, const int32_t* ids, const uint8_t* acts, int64_t n,
+                         int64_t vocab, int n_actions, int d, float* d_item, float* d_action, const EventsBwdWork& w,
+                         cudaStream_t st);
+
+// AdamW over a list of tensors (adamw.cu).
+sa_status adamw_run(const sa_adamw_tensor* tensors, int n_tensors, const sa_adamw_config& c, cudaStream_t st);
+
 // Sums the split-n partials into H (if a.H), the mass and H/(m+eps) (w.Hhat).
 sa_status sa_reduce(const SaFwdArgs& a, const SaFwdWork& w, cudaStream_t st);
 // exponentials per second over the whole GPU: mode 0 all on the MUFU, mode 1 the

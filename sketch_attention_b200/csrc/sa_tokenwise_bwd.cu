@@ -1,0 +1,903 @@
+// Backward of the token-wise normalisation variant (sa_tokenwise.cu): k folded
+// prototypes attend over each user's events, keys = values = X, and the
+// probabilities are recomputed from X.  With U = P W_Q W_K^T / sqrt(d),
+// A = softmax over the user's events of U X^T, H = A X, i = 1/(m + eps):
+//   dW_V = sum_u (i H)^T dS,  dH = i dS W_V^T,  c_j = dH_j . H_j
+//   dZ = A o (dH X^T - c)     (per prototype: both the normaliser and c are row constants)
+//   dX = A^T dH + dZ^T U,  E = sum_u dZ X   (dP, dW_Q, dW_K follow from E by small GEMMs)
+//
+// Accuracy.  dX is bf16; the weight gradients are fp32 and hold fp32-grade
+// accuracy: X is exact in bf16, so the products that feed E take only their
+// other operand (U, dH, dZ) as a bf16 pair hi + lo (16 bits, 2^-17 relative),
+// two tensor-core products each.  The tensor core's fp32 accumulation truncates:
+// a K = 8192 product reads 9e-6 off and drifts with K (85000: 1.6e-5 with signs
+// mixed, 6.6e-5 without), K = 1024 1e-6; so E leaves TMEM every kDrain token
+// tiles (1024 events) and is summed in registers, rounded to nearest.  For dX,
+// Z takes U hi + lo (an error of Z is a relative error of A), the rest bf16.
+//
+// Three tensor-core passes over the events, each bounded by its products
+// (per 128 events x 128 prototypes, 512 clocks per product at the bf16 rate):
+//   tw_lse_kernel  row maximum and sum: 2 products; one CTA per (128-prototype
+//     slice, token chunk), lane = prototype, so a row's statistics stay in a thread.
+//   tw_e_kernel    6 products, same split.  [Z; G] = [U; dH] X^T with lane =
+//     prototype; dZ goes back to TMEM as the A operand of E += dZ X, so nothing
+//     but operands crosses shared memory.
+//   tw_dx_kernel   5 products; one CTA per token chunk, 256 events (two tiles) per
+//     pass over the prototypes (halves the prototype traffic out of L2), lane =
+//     token.  The tiles alternate: while one tile's A and dZ are computed the
+//     tensor core works on the other's.  A and dZ overwrite the logits in TMEM.
+#include <algorithm>
+#include <mutex>
+
+#include "gemm.cuh"
+#include "sa_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tma_map.cuh"
+
+namespace sa {
+
+namespace {
+using namespace tc;
+
+constexpr int TILE = 128, DD = 128;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr uint32_t XT_BYTES = 32768;         // [128 rows x 128] bf16: 2 SW128 halves of 16 KB
+
+// f(t, piece, u, first event, end of the piece, first, last) for every 128-event tile of
+// chunk g, user by user (a piece: the chunk's events of one user)
+template <class F>
+__device__ __forceinline__ void for_each_tile(const int64_t* off, int B, const Chunking& ch, int g, F&& f) {
+  const int64_t cb = (int64_t)g * ch.T, ce = min(cb + ch.T, ch.n_total);
+  int t = 0, piece = 0;
+  for (int u = user_of_token(off, B, cb); u < B && off[u] < ce; ++u) {
+    const int64_t pb = max(off[u], cb), pe = min(off[u + 1], ce);
+    if (pb >= pe) continue;
+    for (int64_t tb = pb; tb < pe; tb += TILE, ++t)
+      if (!f(t, piece, u, tb, pe, tb == pb, tb + TILE >= pe)) return;
+    ++piece;
+  }
+}
+
+__device__ __forceinline__ uint64_t kmajor(uint32_t base, int ks) {
+  return smem_desc(base + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024, SWZ_128B);
+}
+
+// x = hi + lo as bf16 pairs
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(a, b);
+  lo = pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
+}
+
+// waits for this thread's TMEM loads; names their registers, so no use moves above the wait
+template <int N>
+__device__ __forceinline__ void wait_ld(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tmem_wait_ld16(v + i);
+}
+
+__device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row) {
+  tma_load_2d(dst, map, bar, 0, row);
+  tma_load_2d(dst + XT_BYTES / 2, map, bar, 64, row);
+}
+
+// ============================================================== row statistics
+constexpr int S_NXS = 4;
+constexpr uint32_t S_OFF_U = 0;                                  // U hi, U lo
+constexpr uint32_t S_OFF_X = 2 * XT_BYTES;
+constexpr uint32_t S_OFF_BAR = S_OFF_X + S_NXS * XT_BYTES;
+constexpr uint32_t S_SMEM = S_OFF_BAR + 256 + 1024;
+constexpr int S_THREADS = 320;               // warp 0 TMA, 1 MMA, 2-9 two threads per prototype
+
+struct SBars {
+  uint64_t u_full, x_full[S_NXS], x_empty[S_NXS], z_full[2], z_empty[2], mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct SParams {
+  const int64_t* off;
+  int B;
+  Chunking ch;
+  int slices, kp;
+  float2* user;          // [B, 2, kp] (max, sum) of users inside one chunk, by column half
+  float2* slot;          // [G, 2, 2, kp] of the pieces of users that span chunks
+  int* err;
+};
+
+__global__ void __launch_bounds__(S_THREADS, 1)
+    tw_lse_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+                  const __grid_constant__ CUtensorMap tmUlo, SParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  SBars* bars = (SBars*)(smem + S_OFF_BAR);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int sl = blockIdx.x % p.slices, g = blockIdx.x / p.slices;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->u_full, 1);
+    for (int s = 0; s < S_NXS; ++s) { mbar_init(&bars->x_full[s], 1); mbar_init(&bars->x_empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&bars->z_full[b], 1); mbar_init(&bars->z_empty[b], 256); }
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 256);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmX);
+    mbar_arrive_expect_tx(&bars->u_full, 2 * XT_BYTES);
+    load_rows(smem + S_OFF_U, &tmU, &bars->u_full, sl * TILE);
+    load_rows(smem + S_OFF_U + XT_BYTES, &tmUlo, &bars->u_full, sl * TILE);
+    int issued = 0;
+    for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t tb, int64_t, bool, bool) {
+      const int s = t % S_NXS;
+      if (t >= S_NXS && !mbar_wait(&bars->x_empty[s], ((t / S_NXS) - 1) & 1, abort, p.err)) return false;
+      mbar_arrive_expect_tx(&bars->x_full[s], XT_BYTES);
+      load_rows(smem + S_OFF_X + s * XT_BYTES, &tmX, &bars->x_full[s], (int)tb);
+      issued = t + 1;
+      return true;
+    });
+    if (*abort) {                            // no copy may be in flight when the CTA ends
+      mbar_wait_bounded(&bars->u_full, 0);
+      for (int t = std::max(0, issued - S_NXS); t < issued; ++t)
+        mbar_wait_bounded(&bars->x_full[t % S_NXS], (t / S_NXS) & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t id = idesc_bf16(128, 128, false, false);
+    const uint32_t ua = smem_u32(smem + S_OFF_U);
+    if (mbar_wait(&bars->u_full, 0, abort, p.err))
+      for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
+        const int s = t % S_NXS, b = t & 1;
+        if (!mbar_wait(&bars->x_full[s], (t / S_NXS) & 1, abort, p.err)) return false;
+        if (t >= 2 && !mbar_wait(&bars->z_empty[b], ((t >> 1) - 1) & 1, abort, p.err)) return false;
+        tc_fence_after();
+        const uint32_t xa = smem_u32(smem + S_OFF_X + s * XT_BYTES);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_ss(tmem + 128 * b, kmajor(ua, ks), kmajor(xa, ks), id, ks > 0);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_ss(tmem + 128 * b, kmajor(ua + XT_BYTES, ks), kmajor(xa, ks), id, 1u);
+        mma_commit(&bars->z_full[b]);
+        mma_commit(&bars->x_empty[s]);
+        return true;
+      });
+    mma_commit(&bars->mma_done);
+    mbar_wait_bounded(&bars->mma_done, 0);
+  } else if (warp >= 2) {
+    const int q = warp % 4, h = (warp - 2) / 4;          // column half: events 64 h .. 64 h + 63 of a tile
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const int j = sl * TILE + q * 32 + lane;
+    const int64_t cb = (int64_t)g * p.ch.T, ce = min(cb + p.ch.T, p.ch.n_total);
+    float m = -INFINITY, sum = 0.f;
+    for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int u, int64_t tb, int64_t pe, bool first, bool last) {
+      const int b = t & 1;
+      if (first) { m = -INFINITY; sum = 0.f; }
+      if (!mbar_wait(&bars->z_full[b], (t >> 1) & 1, abort, p.err)) return false;
+      tc_fence_after();
+      float z[64];
+      tmem_ld32(tmem + lane_addr + 128 * b + 64 * h, z);
+      tmem_ld32(tmem + lane_addr + 128 * b + 64 * h + 32, z + 32);
+      wait_ld<64>(z);
+      tc_fence_before();
+      mbar_arrive(&bars->z_empty[b]);
+      const int nv = (int)min(pe - tb - 64 * h, (int64_t)64);   // events of this half that are the user's
+      if (nv > 0) {
+        if (nv < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= nv) z[i] = -INFINITY;
+        }
+        float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
+        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+        const float2 nm = make_float2(-mn, -mn);
+        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nm);
+          s2[(i >> 1) & 1] = __fadd2_rn(s2[(i >> 1) & 1], make_float2(ex2(e.x), ex2(e.y)));
+        }
+        sum = fmaf(sum, ex2(m - mn), (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
+        m = mn;
+      }
+      if (last) {
+        const int dest = piece_dest(p.off[u], p.off[u + 1], cb, ce);
+        float2* out = dest == DEST_USER ? p.user + (int64_t)u * 2 * p.kp : p.slot + ((int64_t)g * 2 + dest) * 2 * p.kp;
+        out[(int64_t)h * p.kp + j] = make_float2(m, sum);
+      }
+      return true;
+    });
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// lse2[u, j] = log2 of the row's sum of 2^z over the user's events, from the pieces in chunk
+// order; +inf for a padding prototype (its A = 2^(z - inf) = 0) and for a user without events
+__global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __restrict__ off, int B, Chunking ch, int k,
+                                                             int kp, const float2* __restrict__ user,
+                                                             const float2* __restrict__ slot, float* __restrict__ lse2) {
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < (int64_t)B * kp; r += (int64_t)gridDim.x * 256) {
+    const int u = (int)(r / kp), j = (int)(r % kp);
+    const int64_t ub = off[u], ue = off[u + 1];
+    float lse = INFINITY;
+    if (j < k && ue > ub) {
+      const int64_t gf = ub / ch.T, gl = (ue - 1) / ch.T;
+      float m = -INFINITY, s = 0.f;
+      for (int64_t g = gf; g <= gl; ++g) {
+        const float2* p = gf == gl ? user + (int64_t)u * 2 * kp : slot + (g * 2 + (g == gf ? 1 : 0)) * 2 * kp;
+        for (int h = 0; h < 2; ++h) {
+          const float2 v = p[(int64_t)h * kp + j];
+          if (v.x == -INFINITY && v.y == 0.f) continue;  // a half without events
+          const float mn = fmaxf(m, v.x);
+          s = s * exp2f(m - mn) + v.y * exp2f(v.x - mn);
+          m = mn;
+        }
+      }
+      lse = m + log2f(s);
+    }
+    lse2[r] = lse;
+  }
+}
+
+// ============================================================== E kernel
+constexpr int E_NXS = 3, kDrain = 8;         // token tiles per stay of E in TMEM
+constexpr uint32_t E_OFF_U = 0;                                  // U hi, U lo, dH hi, dH lo
+constexpr uint32_t E_OFF_X = 4 * XT_BYTES;
+constexpr uint32_t E_OFF_BAR = E_OFF_X + E_NXS * XT_BYTES;
+constexpr uint32_t E_SMEM = E_OFF_BAR + 256 + 1024;
+constexpr int E_THREADS = 320;               // warp 0 TMA, 1 MMA, 2-9 two threads per prototype
+constexpr uint32_t E_TM_Z = 0, E_TM_G = 128, E_TM_E = 256, E_TM_DZ = 384;   // dZ: hi 64 columns, lo 64
+
+struct EBars {
+  uint64_t u_full, h_full, h_empty, x_full[E_NXS], x_empty[E_NXS], zg_full, zg_empty, dz_full, e_done, mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct EParams {
+  const int64_t* off;
+  int B;
+  Chunking ch;
+  int slices, k, kp;
+  const float* lse2;     // [B, kp]
+  const float* c;        // [B, kp]
+  float* Epart;          // [G, k, d]
+  int* err;
+};
+
+__global__ void __launch_bounds__(E_THREADS, 1)
+    tw_e_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+                const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH,
+                const __grid_constant__ CUtensorMap tmHlo, EParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  EBars* bars = (EBars*)(smem + E_OFF_BAR);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int sl = blockIdx.x % p.slices, g = blockIdx.x / p.slices;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->u_full, 1);
+    mbar_init(&bars->h_full, 1);
+    mbar_init(&bars->h_empty, 1);
+    for (int s = 0; s < E_NXS; ++s) { mbar_init(&bars->x_full[s], 1); mbar_init(&bars->x_empty[s], 1); }
+    mbar_init(&bars->zg_full, 1);
+    mbar_init(&bars->zg_empty, 256);
+    mbar_init(&bars->dz_full, 256);
+    mbar_init(&bars->e_done, 1);
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmX);
+    mbar_arrive_expect_tx(&bars->u_full, 2 * XT_BYTES);
+    load_rows(smem + E_OFF_U, &tmU, &bars->u_full, sl * TILE);
+    load_rows(smem + E_OFF_U + XT_BYTES, &tmUlo, &bars->u_full, sl * TILE);
+    int issued_x = 0, issued_h = 0;
+    for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int u, int64_t tb, int64_t, bool first, bool) {
+      if (first) {
+        if (piece > 0 && !mbar_wait(&bars->h_empty, (piece - 1) & 1, abort, p.err)) return false;
+        mbar_arrive_expect_tx(&bars->h_full, 2 * XT_BYTES);
+        const int row = (int)((int64_t)u * p.kp + sl * TILE);
+        load_rows(smem + E_OFF_U + 2 * XT_BYTES, &tmH, &bars->h_full, row);
+        load_rows(smem + E_OFF_U + 3 * XT_BYTES, &tmHlo, &bars->h_full, row);
+        issued_h = piece + 1;
+      }
+      const int s = t % E_NXS;
+      if (t >= E_NXS && !mbar_wait(&bars->x_empty[s], ((t / E_NXS) - 1) & 1, abort, p.err)) return false;
+      mbar_arrive_expect_tx(&bars->x_full[s], XT_BYTES);
+      load_rows(smem + E_OFF_X + s * XT_BYTES, &tmX, &bars->x_full[s], (int)tb);
+      issued_x = t + 1;
+      return true;
+    });
+    if (*abort) {
+      mbar_wait_bounded(&bars->u_full, 0);
+      if (issued_h > 0) mbar_wait_bounded(&bars->h_full, (issued_h - 1) & 1);
+      for (int t = std::max(0, issued_x - E_NXS); t < issued_x; ++t)
+        mbar_wait_bounded(&bars->x_full[t % E_NXS], (t / E_NXS) & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t id_zg = idesc_bf16(128, 128, false, false);
+    const uint32_t id_e = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
+    const uint32_t ua = smem_u32(smem + E_OFF_U);
+    auto x_at = [&](int t) { return smem_u32(smem + E_OFF_X + (t % E_NXS) * XT_BYTES); };
+    // E += dZ X of tile t (afresh after every drain)
+    auto emma = [&](int t) -> bool {
+      if (!mbar_wait(&bars->dz_full, t & 1, abort, p.err)) return false;
+      tc_fence_after();
+      const uint32_t xa = x_at(t);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint64_t bx = smem_desc(xa + ks * 2048, 16384, 1024, SWZ_128B);
+        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, bx, id_e, (t % kDrain != 0 || ks > 0) ? 1u : 0u);
+        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, bx, id_e, 1u);
+      }
+      mma_commit(&bars->e_done);
+      mma_commit(&bars->x_empty[t % E_NXS]);
+      return true;
+    };
+    if (mbar_wait(&bars->u_full, 0, abort, p.err)) {
+      int prev = -1;
+      for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int, int64_t, int64_t, bool first, bool last) {
+        if (first && !mbar_wait(&bars->h_full, piece & 1, abort, p.err)) return false;
+        if (!mbar_wait(&bars->x_full[t % E_NXS], (t / E_NXS) & 1, abort, p.err)) return false;
+        if (t > 0 && !mbar_wait(&bars->zg_empty, (t - 1) & 1, abort, p.err)) return false;
+        tc_fence_after();
+        const uint32_t xa = x_at(t);
+#pragma unroll
+        for (int o = 0; o < 4; ++o)                      // Z = (U hi + U lo) X^T, G = (dH hi + dH lo) X^T
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), kmajor(ua + o * XT_BYTES, ks), kmajor(xa, ks), id_zg,
+                   (o & 1) || ks > 0);
+        mma_commit(&bars->zg_full);
+        if (last) mma_commit(&bars->h_empty);
+        if (prev >= 0 && !emma(prev)) return false;
+        prev = t;
+        return true;
+      });
+      if (prev >= 0 && !*abort) emma(prev);
+    }
+    mma_commit(&bars->mma_done);
+    mbar_wait_bounded(&bars->mma_done, 0);
+  } else if (warp >= 2) {
+    const int q = warp % 4, h = (warp - 2) / 4;          // events 64 h .. 64 h + 63 of a tile, columns 64 h .. of E
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const int j = sl * TILE + q * 32 + lane;
+    float acc[64];                                       // this thread's half row of E
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+    auto drain = [&]() {
+#pragma unroll
+      for (int i = 0; i < 64; i += 16) {
+        float v[16];
+        tmem_ld16(tmem + lane_addr + E_TM_E + 64 * h + i, v);
+        tmem_wait_ld16(v);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[i + x] += v[x];
+      }
+    };
+    float2 nl2 = make_float2(0.f, 0.f), nc = make_float2(0.f, 0.f);
+    int tiles = 0;
+    bool ok = true;
+    for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int u, int64_t tb, int64_t pe, bool first, bool) {
+      if (first) {
+        // one event: its probability is 1 whatever Z, so dZ is zero exactly (dA - c would leave
+        // the rounding of two equal numbers)
+        const float l2 = p.off[u + 1] - p.off[u] == 1 ? INFINITY : p.lse2[(int64_t)u * p.kp + j];
+        const float c = p.c[(int64_t)u * p.kp + j];
+        nl2 = make_float2(-l2, -l2);
+        nc = make_float2(-c, -c);
+      }
+      if (!mbar_wait(&bars->zg_full, t & 1, abort, p.err)) return ok = false;
+      tc_fence_after();
+      uint32_t hi[32], lo[32];
+      const int nv = (int)min(pe - tb - 64 * h, (int64_t)64);   // events of this half that are the user's
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float z[32], gv[32];
+        tmem_ld32(tmem + lane_addr + E_TM_Z + 64 * h + 32 * c, z);
+        tmem_ld32(tmem + lane_addr + E_TM_G + 64 * h + 32 * c, gv);
+        wait_ld<32>(z);
+        wait_ld<32>(gv);
+        if (c == 1) {
+          tc_fence_before();
+          mbar_arrive(&bars->zg_empty);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nl2);
+          const float2 d = __fadd2_rn(make_float2(gv[i], gv[i + 1]), nc);
+          float2 dz = __fmul2_rn(make_float2(ex2(e.x), ex2(e.y)), d);
+          if (nv < 64) {
+            if (32 * c + i >= nv) dz.x = 0.f;
+            if (32 * c + i + 1 >= nv) dz.y = 0.f;
+          }
+          split2(dz.x, dz.y, hi[16 * c + i / 2], lo[16 * c + i / 2]);
+        }
+      }
+      // the last tile's E MMA has read dZ, and E is complete up to that tile
+      if (t > 0 && !mbar_wait(&bars->e_done, (t - 1) & 1, abort, p.err)) return ok = false;
+      tc_fence_after();
+      if (t > 0 && t % kDrain == 0) drain();
+      tmem_st32(tmem + lane_addr + E_TM_DZ + 32 * h, hi);
+      tmem_st32(tmem + lane_addr + E_TM_DZ + 64 + 32 * h, lo);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&bars->dz_full);
+      tiles = t + 1;
+      return true;
+    });
+    if (ok && tiles > 0 && mbar_wait(&bars->e_done, (tiles - 1) & 1, abort, p.err)) {
+      tc_fence_after();
+      drain();
+      if (j < p.k) {
+        float* dst = p.Epart + ((int64_t)g * p.k + j) * DD + 64 * h;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) *(float4*)(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ============================================================== dX kernel
+constexpr int KC = 64, X_NCS = 3;            // prototypes per stage, stages
+constexpr uint32_t CH_BYTES = 49152;         // [U h0 | dH h0 | U h1 | dH h1 | Ulo h0 | Ulo h1], 8 KB each
+constexpr uint32_t X_OFF_X = 0;                                  // two token tiles
+constexpr uint32_t X_OFF_CH = 2 * XT_BYTES;
+constexpr uint32_t X_OFF_ROW = X_OFF_CH + X_NCS * CH_BYTES;      // [X_NCS][lse2 64 | ln2 c 64]
+constexpr uint32_t X_OFF_BAR = X_OFF_ROW + X_NCS * 2 * KC * 4;
+constexpr uint32_t X_SMEM = X_OFF_BAR + 256 + 1024;
+constexpr int X_THREADS = 576;               // warp 0 TMA, 1 MMA, 2-9 tile 0 and 10-17 tile 1, two threads per token
+// TMEM columns of tile i: [Z|G] at 128 i, later A and ln2 dZ as bf16 pairs in the columns of Z;
+// dX at 256 + 128 i
+constexpr uint32_t X_TM_ZG = 0, X_TM_Q = 256;
+
+struct XBars {
+  uint64_t x_full[2], x_empty[2], c_full[X_NCS], c_empty[X_NCS], zg_full[2], aa_full[2], q_full[2], mma_done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+struct XParams {
+  const int64_t* off;
+  int B;
+  Chunking ch;
+  int kp;
+  const float* lse2;     // [B, kp]
+  const float* c2;       // [B, kp] ln2 c
+  __nv_bfloat16* dX;     // [n, d]
+  int* err;
+};
+
+// The units of a chunk in order: up to 256 events of one user.
+struct Units {
+  const int64_t* off;
+  int B, u;
+  int64_t ce, tb, pe;                        // the current unit starts at tb, its piece ends at pe
+  __device__ Units(const XParams& p, int g) : off(p.off), B(p.B) {
+    const int64_t cb = (int64_t)g * p.ch.T;
+    ce = min(cb + p.ch.T, p.ch.n_total);
+    u = user_of_token(off, B, cb);
+    tb = cb;
+    pe = min(off[u + 1], ce);
+  }
+  __device__ bool done() const { return tb >= ce; }
+  __device__ bool two() const { return pe - tb > TILE; }
+  __device__ void next() {
+    tb += 2 * TILE;
+    if (tb < pe) return;
+    tb = pe;
+    if (tb >= ce) return;
+    do ++u; while (off[u + 1] <= tb);        // tb < ce <= n: a user with events follows
+    pe = min(off[u + 1], ce);
+  }
+};
+
+__global__ void __launch_bounds__(X_THREADS, 1)
+    tw_dx_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+                 const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH, XParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  XBars* bars = (XBars*)(smem + X_OFF_BAR);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = blockIdx.x, nch = p.kp / KC;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->x_full[i], 1);
+      mbar_init(&bars->x_empty[i], 1);
+      mbar_init(&bars->zg_full[i], 1);
+      mbar_init(&bars->aa_full[i], 256);
+      mbar_init(&bars->q_full[i], 1);
+    }
+    for (int s = 0; s < X_NCS; ++s) { mbar_init(&bars->c_full[s], 1); mbar_init(&bars->c_empty[s], 1); }
+    mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    prefetch_tensormap(&tmX);
+    int cc = 0, tiles[2] = {0, 0};           // stages and tiles issued so far
+    bool ok = true;
+    for (Units un(p, g); ok && !un.done(); un.next()) {
+      const int n_tiles = un.two() ? 2 : 1;
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        if (tiles[i] > 0 && !mbar_wait(&bars->x_empty[i], (tiles[i] - 1) & 1, abort, p.err)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bars->x_full[i], XT_BYTES);
+        load_rows(smem + X_OFF_X + i * XT_BYTES, &tmX, &bars->x_full[i], (int)(un.tb + i * TILE));
+        ++tiles[i];
+      }
+      for (int c = 0; ok && c < nch; ++c, ++cc) {
+        const int s = cc % X_NCS;
+        if (cc >= X_NCS && !mbar_wait(&bars->c_empty[s], ((cc / X_NCS) - 1) & 1, abort, p.err)) { ok = false; break; }
+        mbar_arrive_expect_tx(&bars->c_full[s], CH_BYTES + 2 * KC * 4);
+        uint8_t* cd = smem + X_OFF_CH + s * CH_BYTES;
+        const int64_t row = (int64_t)un.u * p.kp + c * KC;
+        tma_load_2d(cd, &tmU, &bars->c_full[s], 0, c * KC);
+        tma_load_2d(cd + 8192, &tmH, &bars->c_full[s], 0, (int)row);
+        tma_load_2d(cd + 16384, &tmU, &bars->c_full[s], 64, c * KC);
+        tma_load_2d(cd + 24576, &tmH, &bars->c_full[s], 64, (int)row);
+        tma_load_2d(cd + 32768, &tmUlo, &bars->c_full[s], 0, c * KC);
+        tma_load_2d(cd + 40960, &tmUlo, &bars->c_full[s], 64, c * KC);
+        uint8_t* rd = smem + X_OFF_ROW + s * 2 * KC * 4;
+        bulk_load(rd, p.lse2 + row, KC * 4, &bars->c_full[s]);
+        bulk_load(rd + KC * 4, p.c2 + row, KC * 4, &bars->c_full[s]);
+      }
+    }
+    if (*abort) {
+      for (int i = 0; i < 2; ++i)
+        if (tiles[i] > 0) mbar_wait_bounded(&bars->x_full[i], (tiles[i] - 1) & 1);
+      for (int c = std::max(0, cc - X_NCS); c < cc; ++c)
+        mbar_wait_bounded(&bars->c_full[c % X_NCS], (c / X_NCS) & 1);
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t id_zg = idesc_bf16(128, 128, false, false), id_lo = idesc_bf16(128, 64, false, false);
+    const uint32_t id_q = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
+    int xt[2] = {0, 0}, at[2] = {0, 0};      // tiles begun, and stages aggregated, per tile index
+    // [Z|G] of tile i for stage counter cc: Z = X (U hi + U lo)^T, G = X dH^T
+    auto logits = [&](int i, int cc, bool first, bool last) -> bool {
+      if (first) {
+        if (!mbar_wait(&bars->x_full[i], xt[i] & 1, abort, p.err)) return false;
+        ++xt[i];
+      }
+      const int s = cc % X_NCS;
+      if (!mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) return false;
+      tc_fence_after();
+      const uint32_t xa = smem_u32(smem + X_OFF_X + i * XT_BYTES), cb = smem_u32(smem + X_OFF_CH + s * CH_BYTES);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ss(tmem + X_TM_ZG + 128 * i, kmajor(xa, ks), kmajor(cb, ks), id_zg, ks > 0);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        mma_ss(tmem + X_TM_ZG + 128 * i, kmajor(xa, ks),
+               smem_desc(cb + 32768 + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024, SWZ_128B), id_lo, 1u);
+      mma_commit(&bars->zg_full[i]);
+      if (last) mma_commit(&bars->x_empty[i]);
+      return true;
+    };
+    // dX += A dH + (ln2 dZ) U (U in base-2 units) over the stage's 64 prototypes
+    auto aggregate = [&](int i, int cc, bool first, bool last, bool frees) -> bool {
+      if (!mbar_wait(&bars->aa_full[i], at[i] & 1, abort, p.err)) return false;
+      ++at[i];
+      tc_fence_after();
+      const uint32_t cb = smem_u32(smem + X_OFF_CH + (cc % X_NCS) * CH_BYTES);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        // prototypes 16 ks ..: written by the threads of half ks / 2, A then dZ, 16 columns each
+        const uint32_t a = tmem + X_TM_ZG + 128 * i + 32 * (ks >> 1) + 8 * (ks & 1);
+        mma_ts(tmem + X_TM_Q + 128 * i, a, smem_desc(cb + 8192 + ks * 2048, 16384, 1024, SWZ_128B), id_q,
+               (first && ks == 0) ? 0u : 1u);
+        mma_ts(tmem + X_TM_Q + 128 * i, a + 16, smem_desc(cb + ks * 2048, 16384, 1024, SWZ_128B), id_q, 1u);
+      }
+      if (frees) mma_commit(&bars->c_empty[cc % X_NCS]);
+      if (last) mma_commit(&bars->q_full[i]);
+      return true;
+    };
+    int cc = 0;
+    Units un(p, g), nx(p, g);
+    bool ok = !un.done() && logits(0, 0, true, nch == 1) && (!un.two() || logits(1, 0, true, nch == 1));
+    while (ok && !un.done()) {
+      nx.next();
+      const bool two = un.two();
+      for (int c = 0; ok && c < nch; ++c, ++cc) {
+        const bool last = c == nch - 1;
+        // what follows this stage: the unit's next prototypes, or the next unit's first
+        const bool more = !last || !nx.done(), next_two = last ? (!nx.done() && nx.two()) : two;
+        const bool nf = last, nl = last ? nch == 1 : c + 1 == nch - 1;
+        // a unit of one tile is followed by one of two only across units: tile 1's logits then
+        // have no aggregation before them
+        ok = aggregate(0, cc, c == 0, last, !two) && (!more || logits(0, cc + 1, nf, nl)) &&
+             (!two || aggregate(1, cc, c == 0, last, true)) && (!next_two || logits(1, cc + 1, nf, nl));
+      }
+      un.next();
+    }
+    mma_commit(&bars->mma_done);
+    mbar_wait_bounded(&bars->mma_done, 0);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------------ two threads per token
+    const int q = warp % 4, i = (warp - 2) / 8, h = ((warp - 2) / 4) & 1;
+    const int row = q * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    const uint32_t own = tmem + lane_addr + X_TM_ZG + 128 * i + 32 * h;   // Z of prototypes 32 h .. 32 h + 31
+    const float2 ln2v = make_float2(kLn2, kLn2);
+    int cc = 0, a = 0, t = 0;                // stage counter; stages and units of this thread's tile
+    bool ok = true;
+    for (Units un(p, g); ok && !un.done(); un.next()) {
+      if (i == 1 && !un.two()) {
+        cc += nch;
+        continue;
+      }
+      for (int c = 0; c < nch; ++c, ++cc, ++a) {
+        const int s = cc % X_NCS;
+        if (!mbar_wait(&bars->zg_full[i], a & 1, abort, p.err) ||
+            !mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) { ok = false; break; }
+        tc_fence_after();
+        float z[32], gv[32];
+        tmem_ld32(own, z);
+        tmem_ld32(own + 64, gv);
+        wait_ld<32>(z);
+        wait_ld<32>(gv);
+        const float4* l4 = (const float4*)(smem + X_OFF_ROW + s * 2 * KC * 4) + 8 * h;
+        const float4* c4 = l4 + KC / 4;
+        uint32_t pk[32];                     // A in 0..15, ln2 dZ in 16..31 (even prototype low)
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const float4 l = l4[b], cv = c4[b];
+          const float2 lp[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
+          const float2 cp[2] = {make_float2(-cv.x, -cv.y), make_float2(-cv.z, -cv.w)};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int j = 4 * b + 2 * x;
+            const float2 e = __fadd2_rn(make_float2(z[j], z[j + 1]), lp[x]);
+            const float2 A = make_float2(ex2(e.x), ex2(e.y));
+            const float2 dz = __fmul2_rn(A, __ffma2_rn(make_float2(gv[j], gv[j + 1]), ln2v, cp[x]));
+            pk[j / 2] = pack_bf16x2(A.x, A.y);
+            pk[16 + j / 2] = pack_bf16x2(dz.x, dz.y);
+          }
+        }
+        tmem_st32(own, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->aa_full[i]);
+      }
+      if (!ok) break;
+      // this thread's 64 columns of the token's dX
+      if (!mbar_wait(&bars->q_full[i], t & 1, abort, p.err)) { ok = false; break; }
+      tc_fence_after();
+      const int64_t r = un.tb + i * TILE + row;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float v[32];
+        tmem_ld32(tmem + lane_addr + X_TM_Q + 128 * i + 64 * h + 32 * b, v);
+        wait_ld<32>(v);
+        if (r < un.pe) {
+          uint4* dst = (uint4*)(p.dX + r * DD + 64 * h + 32 * b);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            dst[x] = make_uint4(pack_bf16x2(v[8 * x], v[8 * x + 1]), pack_bf16x2(v[8 * x + 2], v[8 * x + 3]),
+                                pack_bf16x2(v[8 * x + 4], v[8 * x + 5]), pack_bf16x2(v[8 * x + 6], v[8 * x + 7]));
+        }
+      }
+      tc_fence_before();                     // read before this thread's next arrival at aa_full
+      ++t;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ============================================================== operands
+// Rows 0 .. kp of the first part: U (base-2 units) as hi + lo, zero rows behind k.  Then, per
+// user and prototype, dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c (a user without events and
+// padding prototypes: zeros).  A warp computes four rows at once from W_V^T in shared memory.
+constexpr int PREP_THREADS = 256, PREP_WARPS = PREP_THREADS / 32;
+constexpr int PREP_SMEM = (DD * (DD + 1) + PREP_WARPS * 4 * DD) * 4;
+
+__global__ void __launch_bounds__(PREP_THREADS) tw_prepare_kernel(
+    const int64_t* __restrict__ off, int B, int k, int kp, float inv, const float* __restrict__ Pf,
+    const float* __restrict__ W_V, const float* __restrict__ dS, const float* __restrict__ H,
+    __nv_bfloat16* __restrict__ Uhi, __nv_bfloat16* __restrict__ Ulo, __nv_bfloat16* __restrict__ Hhi,
+    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2) {
+  extern __shared__ float sm[];
+  float* wt = sm;                                       // wt[e * 129 + d] = W_V[d, e]
+  float* rows = sm + DD * (DD + 1);                     // [warp][4][DD] rows of dS
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  for (int e = threadIdx.x; e < DD * DD; e += PREP_THREADS) wt[(e % DD) * (DD + 1) + e / DD] = W_V[e];
+  __syncthreads();
+  for (int64_t e = (int64_t)blockIdx.x * PREP_THREADS + threadIdx.x; e < (int64_t)kp * DD;
+       e += (int64_t)gridDim.x * PREP_THREADS) {
+    const float x = e < (int64_t)k * DD ? Pf[e] : 0.f;
+    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+    Uhi[e] = hi;
+    Ulo[e] = __float2bfloat16_rn(x - __bfloat162float(hi));
+  }
+  float* mine = rows + warp * 4 * DD;
+  const int64_t groups = (int64_t)B * (kp / 4);
+  for (int64_t gr = (int64_t)blockIdx.x * PREP_WARPS + warp; gr < groups; gr += (int64_t)gridDim.x * PREP_WARPS) {
+    const int u = (int)(gr / (kp / 4)), j0 = (int)(gr % (kp / 4)) * 4;
+    const bool some = off[u + 1] > off[u];
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        mine[r * DD + 32 * x + lane] =
+            some && j0 + r < k ? dS[((int64_t)u * k + j0 + r) * DD + 32 * x + lane] : 0.f;
+    __syncwarp();
+    float acc[4][4] = {};
+    for (int e = 0; e < DD; e += 4) {
+      float4 s[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r] = *(const float4*)(mine + r * DD + e);
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float w = wt[(e + y) * (DD + 1) + 32 * x + lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[r][x] = fmaf((&s[r].x)[y], w, acc[r][x]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int64_t in = ((int64_t)u * k + j0 + r) * DD, out = ((int64_t)u * kp + j0 + r) * DD;
+      float dot = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float v = acc[r][x] * inv;
+        if (some && j0 + r < k) dot = fmaf(v, H[in + 32 * x + lane], dot);
+        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+        Hhi[out + 32 * x + lane] = hi;
+        Hlo[out + 32 * x + lane] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      }
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) {
+        cj[(int64_t)u * kp + j0 + r] = dot;
+        c2[(int64_t)u * kp + j0 + r] = kLn2 * dot;
+      }
+    }
+  }
+}
+
+int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
+
+// token chunks of the per-slice kernels: one CTA per (slice, chunk), one wave
+Chunking slice_chunks(int64_t n, int k) {
+  return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
+}
+Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
+
+sa_status map_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_rows) {
+  return tma_map_bf16(map, base, DD, (uint64_t)rows, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+}  // namespace
+
+size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, TokenwiseBwdWork* w) {
+  Carve c(base);
+  TokenwiseBwdWork v;
+  const size_t kp = padded_k(k), kd = (size_t)k * d, dd = (size_t)d * d;
+  v.chE = slice_chunks(n, k);
+  v.chX = token_chunks(n);
+  const size_t G = (size_t)std::max(v.chE.G, 1);
+  v.T = c.take<float>(dd);
+  v.Pf = c.take<float>(kd);
+  for (__nv_bfloat16** p : {&v.Uhi, &v.Ulo}) *p = c.take<__nv_bfloat16>(kp * d);
+  for (__nv_bfloat16** p : {&v.Hhi, &v.Hlo}) *p = c.take<__nv_bfloat16>((size_t)B * kp * d);
+  for (float** p : {&v.c, &v.c2, &v.lse2}) *p = c.take<float>((size_t)B * kp);
+  v.stat_user = c.take<float2>((size_t)B * 2 * kp);
+  v.stat_slot = c.take<float2>(G * 4 * kp);
+  v.Epart = c.take<float>(G * kd);
+  for (float** p : {&v.E, &v.dQ, &v.Q}) *p = c.take<float>(kd);
+  v.gsplit = c.take<float>((size_t)kMaxSplit * dd);
+  if (w) *w = v;
+  return c.bytes();
+}
+
+sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st) {
+  static unsigned long long done_s = 0, done_e = 0, done_x = 0, done_p = 0;
+  static std::mutex mu;
+  set_smem_limit_once((const void*)tw_lse_kernel, S_SMEM, &done_s, mu);
+  set_smem_limit_once((const void*)tw_e_kernel, E_SMEM, &done_e, mu);
+  set_smem_limit_once((const void*)tw_dx_kernel, X_SMEM, &done_x, mu);
+  set_smem_limit_once((const void*)tw_prepare_kernel, PREP_SMEM, &done_p, mu);
+  const int kp = padded_k(a.k), slices = kp / TILE;
+  const float inv = 1.f / (1.f + a.eps);                // m = 1 for a user with events
+  sa_status s;
+  // dW_V = i sum_u H^T dS
+  Gemm gv;
+  gv.M = a.d; gv.N = a.d; gv.K = a.B * a.k;
+  gv.A = a.H; gv.lda = a.d; gv.transA = true;
+  gv.B = a.dS; gv.ldb = a.d;
+  gv.C = a.dW_V; gv.ldc = a.d; gv.alpha = inv; gv.tag = "gemm:dW_V";
+  gv.split_k = gemm_split_for(a.d, a.d, gv.K, kMaxSplit);
+  gv.split_ws = w.gsplit;
+  if ((s = gemm(gv, st)) != SA_OK) return s;
+  if (a.n_total > 0) {
+    if ((s = sa_fold(a.k, a.d, a.P, a.W_Q, a.W_K, w.T, w.Pf, nullptr, st)) != SA_OK) return s;
+    const int64_t warps = std::max<int64_t>((int64_t)a.B * (kp / 4), 1);
+    const unsigned prep = (unsigned)std::min<int64_t>((warps + PREP_WARPS - 1) / PREP_WARPS, 2 * device_info().sm_count);
+    SA_TIMED("tw_prepare_kernel", st,
+             (tw_prepare_kernel<<<prep, PREP_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, w.Pf, a.W_V, a.dS,
+                                                                       a.H, w.Uhi, w.Ulo, w.Hhi, w.Hlo, w.c, w.c2)));
+    CUtensorMap tmX, tmU, tmUlo, tmH, tmHlo, tmU64, tmUlo64, tmH64;
+    const int64_t hrows = (int64_t)a.B * kp;
+    if ((s = map_rows(&tmX, a.X, a.n_total, 128)) != SA_OK) return s;
+    if ((s = map_rows(&tmU, w.Uhi, kp, 128)) != SA_OK) return s;
+    if ((s = map_rows(&tmUlo, w.Ulo, kp, 128)) != SA_OK) return s;
+    if ((s = map_rows(&tmH, w.Hhi, hrows, 128)) != SA_OK) return s;
+    if ((s = map_rows(&tmHlo, w.Hlo, hrows, 128)) != SA_OK) return s;
+    if ((s = map_rows(&tmU64, w.Uhi, kp, 64)) != SA_OK) return s;
+    if ((s = map_rows(&tmUlo64, w.Ulo, kp, 64)) != SA_OK) return s;
+    if ((s = map_rows(&tmH64, w.Hhi, hrows, 64)) != SA_OK) return s;
+    SParams sp{a.off_dev, a.B, w.chE, slices, kp, w.stat_user, w.stat_slot, device_status_word()};
+    SA_TIMED("tw_lse_kernel", st,
+             (tw_lse_kernel<<<w.chE.G * slices, S_THREADS, S_SMEM, st>>>(tmX, tmU, tmUlo, sp)));
+    SA_TIMED("tw_lse_combine_kernel", st,
+             (tw_lse_combine_kernel<<<(unsigned)std::min<int64_t>((hrows + 255) / 256, 4096), 256, 0, st>>>(
+                 a.off_dev, a.B, w.chE, a.k, kp, w.stat_user, w.stat_slot, w.lse2)));
+    XParams xp{a.off_dev, a.B, w.chX, kp, w.lse2, w.c2, (__nv_bfloat16*)a.dX, device_status_word()};
+    SA_TIMED("tw_dx_kernel", st, (tw_dx_kernel<<<w.chX.G, X_THREADS, X_SMEM, st>>>(tmX, tmU64, tmUlo64, tmH64, xp)));
+    EParams ep{a.off_dev, a.B, w.chE, slices, a.k, kp, w.lse2, w.c, w.Epart, device_status_word()};
+    SA_TIMED("tw_e_kernel", st,
+             (tw_e_kernel<<<w.chE.G * slices, E_THREADS, E_SMEM, st>>>(tmX, tmU, tmUlo, tmH, tmHlo, ep)));
+  }
+  SaBwdWork gw{};
+  gw.chE = w.chE;
+  gw.Epart = w.Epart;
+  gw.E = w.E;
+  gw.dQ = w.dQ;
+  gw.Q = w.Q;
+  gw.gsplit = w.gsplit;
+  return sa_bwd_weight_grads(a, gw, st);
+}
+
+}  // namespace sa

@@ -1,0 +1,117 @@
+"""GPU checks of sa_gather_events_backward against the fp64 oracle: the sum of c fp32 terms
+in any order is off by at most c 2^-24 of the sum of their absolute values."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(n, vocab, actions, d, dtype, seed, ids=None):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, vocab, (n,), generator=g) if ids is None else ids
+    acts = torch.randint(0, actions, (n,), generator=g)
+    return ids.int().cuda(), acts.to(torch.uint8).cuda(), torch.randn(n, d, generator=g).to(dtype).cuda()
+
+
+def _check(lib, ids, acts, dX, vocab, actions, **kw):
+    got = lib.sa_gather_events_backward(ids, acts, dX, vocab, actions, **kw)
+    torch.cuda.synchronize()
+    i, a, x = ids.cpu().numpy(), acts.cpu().numpy(), dX.double().cpu().numpy()
+    ones = np.ones((len(i), 1))
+    for name, ref, size, cnt in zip(("d_item", "d_action"), oracle.event_table_grads(i, a, x, vocab, actions),
+                                    oracle.event_table_grads(i, a, np.abs(x), vocab, actions),
+                                    oracle.event_table_grads(i, a, ones, vocab, actions)):
+        err = np.abs(got[name].double().cpu().numpy() - ref)
+        assert err.shape == ref.shape
+        assert (err <= cnt * 2.0 ** -24 * size).all(), (name, err.max())
+    return got
+
+
+# n, vocab, actions, d: one event; sizes around a warp, a list piece (256), a CTA's share; one-row
+# tables; more and fewer rows than a CTA takes; widths below, at and above a warp's 128 columns
+CASES = [(1, 1, 1, 128), (31, 5, 2, 128), (257, 7, 8, 128), (1000, 1000, 3, 128), (1025, 200_000, 8, 128),
+         (4097, 1023, 8, 128), (20_000, 1024, 16, 128), (50_001, 70_000, 8, 128), (3000, 300, 256, 128),
+         (700, 90, 9, 8), (700, 90, 9, 64), (700, 90, 9, 200), (5000, 3, 2, 264)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n,vocab,actions,d", CASES)
+def test_against_the_oracle(lib, n, vocab, actions, d, dtype):
+    _check(lib, *_inputs(n, vocab, actions, d, dtype, n + d), vocab, actions)
+    lib.poll_device_status()
+
+
+@pytest.mark.parametrize("n,shares", [(70_000, (1.0,)), (70_001, (0.5, 0.5)), (40_000, (0.9, 0.05)), (600, (0.5,)),
+                                      (33, (1.0,)), (512, (1.0,)), (768, (0.33, 0.34))])
+def test_popular_items(lib, n, shares):
+    """Items with long runs (inside, at and across the 256-event pieces) beside rare ones."""
+    vocab = 5000
+    g = torch.Generator().manual_seed(n)
+    ids = torch.randint(0, vocab, (n,), generator=g)
+    at = 0
+    for k, s in enumerate(shares):
+        ids[at:at + int(n * s)] = 17 + 64 * k
+        at += int(n * s)
+    ids = ids[torch.randperm(n, generator=g)]
+    _check(lib, *_inputs(n, vocab, 8, 128, torch.bfloat16, 3, ids=ids), vocab, 8)
+
+
+def test_events_outside_the_tables_count_for_neither(lib):
+    ids, acts, dX = _inputs(3000, 500, 8, 128, torch.bfloat16, 4)
+    ids[7], ids[8], ids[9] = -1, 500, 2 ** 31 - 1
+    ids[10] = -2 ** 31
+    acts[11], acts[12] = 8, 255
+    dX[7:13] = float("nan")                       # their gradient must not reach any sum
+    _check_nan = lib.sa_gather_events_backward(ids, acts, dX, 500, 8)
+    torch.cuda.synchronize()
+    assert all(bool(t.isfinite().all()) for t in _check_nan.values())
+    with pytest.raises(lib.SAError):
+        lib.poll_device_status()
+    lib.poll_device_status()
+    dX[7:13] = 1.0
+    _check(lib, ids, acts, dX, 500, 8)
+    for only in ("want_item", "want_action"):     # each table alone reports them too
+        lib.sa_gather_events_backward(ids, acts, dX, 500, 8, **{only: False})
+        with pytest.raises(lib.SAError):
+            lib.poll_device_status()
+
+
+def test_no_events_and_one_table(lib):
+    ids, acts, dX = _inputs(0, 40, 3, 128, torch.float32, 5)
+    got = lib.sa_gather_events_backward(ids, acts, dX, 40, 3)
+    assert all(torch.count_nonzero(t) == 0 for t in got.values())
+    ids, acts, dX = _inputs(900, 40, 3, 128, torch.float32, 6)
+    both = lib.sa_gather_events_backward(ids, acts, dX, 40, 3)
+    item = lib.sa_gather_events_backward(ids, acts, dX, 40, 3, want_action=False)
+    action = lib.sa_gather_events_backward(ids, acts, dX, 40, 3, want_item=False)
+    assert set(item) == {"d_item"} and set(action) == {"d_action"}
+    assert torch.equal(item["d_item"], both["d_item"]) and torch.equal(action["d_action"], both["d_action"])
+
+
+def test_the_same_bits_twice_captured_and_only_the_outputs_written(lib):
+    n, vocab = 30_000, 2000
+    g = torch.Generator().manual_seed(1)
+    hot = torch.where(torch.rand(n, generator=g) < 0.3, torch.full((n,), 5), torch.randint(0, vocab, (n,), generator=g))
+    ids, acts, dX = _inputs(n, vocab, 8, 128, torch.bfloat16, 7, ids=hot)
+    first = lib.sa_gather_events_backward(ids, acts, dX, vocab, 8)
+    size, guard = lib.sa_gather_events_backward_workspace(n, vocab, 8, 128), 256
+    ws = torch.full((size + guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    item = torch.full((vocab * 128 + guard,), 7.0, device="cuda")
+    action = torch.full((8 * 128 + guard,), 7.0, device="cuda")
+    out = {"d_item": item[:-guard].view(vocab, 128), "d_action": action[:-guard].view(8, 128)}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lib.sa_gather_events_backward(ids, acts, dX, vocab, 8, out=out, workspace=ws[:size])
+    for _ in range(2):
+        graph.replay()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = lib.sa_gather_events_backward(ids, acts, dX, vocab, 8, stream=side)
+    torch.cuda.synchronize()
+    for name in first:
+        assert torch.equal(first[name], out[name]) and torch.equal(first[name], other[name])
+    assert bool((item[-guard:] == 7.0).all()) and bool((action[-guard:] == 7.0).all())
+    assert bool((ws[size:] == 0x5A).all())

@@ -151,8 +151,9 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
 struct EventsBwdWork {
   uint32_t *keys[2], *events[2];   // [n] sorted item ids and their events, in two buffers
   int* hist;             // [sort CTAs, 1024] digit counts
-  float* pieces;         // [n / 256, d] sums of list pieces that one item fills
-  float* action_part;    // [action CTAs, n_actions, d]
+  unsigned* seen;        // a bit per item: it has events
+  float *first, *last;   // [n / 64, d] sums of the runs that cross a window's begin and end
+  float* action_part;    // [CTAs, n_actions, d]
 };
 size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, int d, EventsBwdWork* w);
 sa_status events_bwd_run(const void* dX, sa_dtype dtype, const int32_t* ids, const uint8_t* acts, int64_t n,

@@ -88,7 +88,11 @@ def test_no_events_and_one_table(lib):
     item = lib.sa_gather_events_backward(ids, acts, dX, 40, 3, want_action=False)
     action = lib.sa_gather_events_backward(ids, acts, dX, 40, 3, want_item=False)
     assert set(item) == {"d_item"} and set(action) == {"d_action"}
-    assert torch.equal(item["d_item"], both["d_item"]) and torch.equal(action["d_action"], both["d_action"])
+    assert torch.equal(item["d_item"], both["d_item"])
+    # alone, the action sums run in the events' order, not the items': 2 c 2^-24 of the absolute sums
+    size = oracle.event_table_grads(ids.cpu().numpy(), acts.cpu().numpy(), dX.abs().cpu().numpy(), 40, 3)[1]
+    err = (action["d_action"] - both["d_action"]).abs().double().cpu().numpy()
+    assert (err <= 2 * 900 * 2.0 ** -24 * size).all()
 
 
 def test_the_same_bits_twice_captured_and_only_the_outputs_written(lib):

@@ -8,16 +8,17 @@
 // The rows are ordered by item id with a stable radix sort of (id, event) pairs (an
 // LSD pass per kMaxBits bits of the vocabulary's size: two for a million items), so
 // every table row's gradient is the sum of a contiguous run of the list, in the order
-// of the events.  The list is cut into windows of 64 positions, one per warp: runs
-// inside a window are written at once, the sums of the runs that cross its ends are
-// kept, and a second kernel adds those.  So every row of dX is read once and every
-// warp has the same work however popular an item is (under Zipf(1.1) ids over a
-// million items one item has 1 event in 8).  The same pass adds each row to its
-// action's sum, in a table per warp in shared memory.
+// of the events.  The list is cut into equal windows, one per half-warp: runs inside a
+// window are written at once, the sums of the runs that cross its ends are kept, and a
+// second kernel adds those.  So every row of dX is read once and every half-warp has
+// the same work however popular an item is (under Zipf(1.1) ids over a million items
+// one item has 1 event in 8).  The same pass adds each row to its action's sum, in a
+// table per half-warp in shared memory.
 //
 // Bound by memory: dX read once, the item gradient written once.  Most of it is zero
-// rows (a million items, 680K events); they are written by extra CTAs of the sort's
-// kernels, which by themselves wait on latency and leave the memory idle.
+// rows (a million items, 680K events): extra CTAs of the sort's kernels, which by
+// themselves wait on latency and leave the memory idle, zero the whole table (512 MB
+// under 60 us of sorting); the rows with events are written over that.
 #include <algorithm>
 #include <mutex>
 
@@ -30,9 +31,11 @@ namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kSmallN = 4096;                // events that one CTA sorts in one launch
-constexpr int kWin = 64;                     // list positions per window
-constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
-constexpr int kLong = 32;                    // windows of a run that one warp adds; longer: the whole CTA
+constexpr int kMinWin = 32;                  // list positions per window, at least
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32, kHalves = 2 * kSumWarps;
+constexpr int kCols = 8;                     // columns per lane: a half-warp covers 128
+constexpr int kBatch = 8;                    // rows in flight per half-warp
+constexpr int kLong = 32;                    // windows of a run that one half-warp adds; longer: the whole CTA
 constexpr int kFusedActions = 16;            // action tables that the window kernel keeps in shared memory
 
 struct Pass {
@@ -66,51 +69,46 @@ struct FromList {
   __device__ bool outside(uint32_t) const { return false; }
 };
 
-// hist[CTA][bin]: the CTA's events with each digit.  The first pass also marks the items that
-// have events in `seen` (a bit per item).
+// `count` 16-byte pieces from `out` on, zeroed by CTA `cta` of `ctas`
+struct ZeroPart {
+  float4* out;
+  int64_t count;
+};
+__device__ __forceinline__ void zero_part(const ZeroPart& z, int cta, int ctas) {
+  const int64_t stride = (int64_t)ctas * blockDim.x;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int64_t i = (int64_t)cta * blockDim.x + threadIdx.x; i < z.count; i += stride) __stcs(z.out + i, zero);
+}
+
+// hist[CTA][bin]: the CTA's events with each digit.  CTAs from `ctas` on zero their part.
 template <class In>
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(In in, Pass ps, int* __restrict__ hist,
-                                                                  unsigned* __restrict__ seen, int* err) {
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(In in, Pass ps, int ctas, int* __restrict__ hist,
+                                                                  ZeroPart z, int* err) {
   __shared__ int cnt[1 << kMaxBits];
+  if ((int)blockIdx.x >= ctas) {
+    zero_part(z, (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
+    return;
+  }
   const int bins = 1 << ps.bits;
   for (int b = threadIdx.x; b < bins; b += kSortThreads) cnt[b] = 0;
   __syncthreads();
   const int64_t begin = (int64_t)blockIdx.x * ps.per, end = min(begin + ps.per, ps.n);
-  for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) {
-    const uint32_t key = in.key(i);
-    atomicAdd(&cnt[(key >> ps.shift) & (bins - 1)], 1);
-    if (in.outside(key)) {
-      atomicOr(err, DEV_ERR_INDEX);
-    } else if (seen) {
-      const unsigned bit = 1u << (key & 31);
-      if (!(__ldcg(seen + (key >> 5)) & bit)) atomicOr(seen + (key >> 5), bit);
-    }
+  bool bad = false;
+  for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += 4 * kSortThreads) {
+    uint32_t key[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) key[q] = i0 + q * kSortThreads < end ? in.key(i0 + q * kSortThreads) : 0u;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i0 + q * kSortThreads < end) {
+        bad |= in.outside(key[q]);
+        atomicAdd(&cnt[(key[q] >> ps.shift) & (bins - 1)], 1);
+      }
   }
+  if (bad) atomicOr(err, DEV_ERR_INDEX);
   __syncthreads();
   for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[(int64_t)blockIdx.x * bins + b] = cnt[b];
-}
-
-// Zero rows of the item gradient that no event names: table rows [begin, end), `d` floats each,
-// spread over the CTA's and its peers' warps; with seen = NULL all of them.
-struct ZeroRows {
-  float* out;
-  const unsigned* seen;
-  int64_t begin, end;
-  int d;
-};
-__device__ __forceinline__ void zero_rows(const ZeroRows& z, int cta, int ctas) {
-  const int lane = threadIdx.x % 32;
-  const int64_t warp = (int64_t)cta * (blockDim.x / 32) + threadIdx.x / 32, warps = (int64_t)ctas * (blockDim.x / 32);
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  // 32 rows (one word of `seen`) at a time
-  for (int64_t w = z.begin / 32 + warp; w * 32 < z.end; w += warps) {
-    const unsigned have = z.seen ? z.seen[w] : 0u;
-    const int64_t r0 = w * 32, r1 = min(r0 + 32, z.end);
-    for (int64_t r = max(r0, z.begin); r < r1; ++r) {
-      if ((have >> (r - r0)) & 1) continue;
-      for (int c = lane * 4; c < z.d; c += 128) *(float4*)(z.out + r * z.d + c) = zero;
-    }
-  }
 }
 
 // Shared memory of a sorting CTA: wcnt [kSortWarps][bins], base [bins], half [2][bins]
@@ -217,28 +215,28 @@ __device__ void place(const In& in, const Pass& ps, int cta, int ctas, const int
   }
 }
 
-// CTAs [0, ctas) sort, the others write zero rows
+// CTAs [0, ctas) sort, the others zero their part
 template <class In>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(In in, Pass ps, int ctas, const int* __restrict__ hist,
                                                                   uint32_t* __restrict__ keys,
-                                                                  uint32_t* __restrict__ events, ZeroRows z) {
+                                                                  uint32_t* __restrict__ events, ZeroPart z) {
   extern __shared__ __align__(16) int smem[];
   if ((int)blockIdx.x >= ctas) {
-    zero_rows(z, (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
+    zero_part(z, (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
     return;
   }
   place(in, ps, (int)blockIdx.x, ctas, hist, smem, keys, events);
 }
 
-// All passes of a short list in CTA 0 (into buffer (passes - 1) & 1); the others write zero rows
+// All passes of a short list in CTA 0 (into buffer (passes - 1) & 1); the others zero their part
 struct Buffers {
   uint32_t *keys[2], *events[2];
 };
 __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(FromEvents in, int64_t n, int bits, int passes,
-                                                                  Buffers buf, ZeroRows z, int* err) {
+                                                                  Buffers buf, ZeroPart z, int* err) {
   extern __shared__ __align__(16) int smem[];
   if (blockIdx.x > 0) {
-    zero_rows(z, (int)blockIdx.x - 1, (int)gridDim.x - 1);
+    zero_part(z, (int)blockIdx.x - 1, (int)gridDim.x - 1);
     return;
   }
   for (int64_t i = threadIdx.x; i < n; i += kSortThreads)
@@ -256,231 +254,312 @@ __global__ void __launch_bounds__(kSortThreads) sort_small_kernel(FromEvents in,
   }
 }
 
-__device__ __forceinline__ float4 row4(const __nv_bfloat16* p) {
-  const uint2 w = *(const uint2*)p;
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+// 8 columns of a row, as they lie in memory
+struct RawB {
+  uint4 w;
+};
+struct RawF {
+  float4 a, b;
+};
+__device__ __forceinline__ RawB load_raw(const __nv_bfloat16* p) { return {__ldcs((const uint4*)p)}; }
+__device__ __forceinline__ RawF load_raw(const float* p) {
+  return {__ldcs((const float4*)p), __ldcs((const float4*)p + 1)};
 }
-__device__ __forceinline__ float4 row4(const float* p) { return *(const float4*)p; }
-__device__ __forceinline__ void add4(float4& a, const float4& b) {
-  a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+struct Cols {                                // 8 fp32 columns, added in pairs
+  float2 x[4];
+};
+__device__ __forceinline__ Cols widen(const RawB& r) {
+  const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+  Cols c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c.x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return c;
+}
+__device__ __forceinline__ Cols widen(const RawF& r) {
+  return {{make_float2(r.a.x, r.a.y), make_float2(r.a.z, r.a.w), make_float2(r.b.x, r.b.y), make_float2(r.b.z, r.b.w)}};
+}
+__device__ __forceinline__ Cols zero_cols() {
+  const float2 z = make_float2(0.f, 0.f);
+  return {{z, z, z, z}};
+}
+__device__ __forceinline__ void add_cols(Cols& a, const Cols& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a.x[i] = __fadd2_rn(a.x[i], b.x[i]);
+}
+__device__ __forceinline__ Cols load_cols(const float* p) {
+  const float4 a = *(const float4*)p, b = *((const float4*)p + 1);
+  return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+}
+__device__ __forceinline__ void store_cols(float* p, const Cols& c) {
+  *(float4*)p = make_float4(c.x[0].x, c.x[0].y, c.x[1].x, c.x[1].y);
+  *((float4*)p + 1) = make_float4(c.x[2].x, c.x[2].y, c.x[3].x, c.x[3].y);
 }
 
-// Window w is list positions [kWin w, kWin (w + 1)).  A warp walks its windows row by row: a run
+// A half-warp's table of action sums in shared memory: [n_actions][2][16 lanes] float4, so that the
+// lanes' 16-byte accesses are consecutive
+struct Table {
+  float4* base;
+  __device__ void clear(int n_actions, int l) const {
+    for (int a = 0; a < 2 * n_actions; ++a) base[a * 16 + l] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ void add(int a, int l, const Cols& c) const {
+    float4* p = base + a * 32 + l;
+    float4 u = p[0], v = p[16];
+    u.x += c.x[0].x; u.y += c.x[0].y; u.z += c.x[1].x; u.w += c.x[1].y;
+    v.x += c.x[2].x; v.y += c.x[2].y; v.z += c.x[3].x; v.w += c.x[3].y;
+    p[0] = u;
+    p[16] = v;
+  }
+};
+// the CTA's tables, added in order, to out[n_actions][d] (columns c0 .. c0 + 127 of it)
+__device__ __forceinline__ void store_tables(const float4* tables, int count, int n_actions, int c0, int d, float* out) {
+  for (int e = threadIdx.x; e < n_actions * 32; e += blockDim.x) {
+    const int col = c0 + (e % 16) * kCols + (e / 16) % 2 * 4;
+    float4 acc = tables[e];
+    for (int h = 1; h < count; ++h) {
+      const float4 x = tables[h * n_actions * 32 + e];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    if (col < d) *(float4*)(out + (int64_t)(e / 32) * d + col) = acc;
+  }
+}
+
+// What a window leaves for the second kernel: its first key, and the key of its last run if that
+// starts in it and goes on behind it (else kNone).
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// Window w is list positions [win w, win (w + 1)), a half-warp's.  It walks them row by row: a run
 // that lies inside is written to its table row; the sum before the window's first run head goes to
 // first[w], that of a run which goes on behind the window to last[w].  With kActions every row is
-// also added to the warp's table of action sums; the CTA's tables are added in order at the end,
-// into action_part[CTA][n_actions][d].
+// also added to the half-warp's table of action sums; the CTA's tables go to
+// action_part[CTA][n_actions][d].
 template <class T, bool kActions>
 __global__ void __launch_bounds__(kSumThreads) window_rows_kernel(const T* __restrict__ dX,
                                                                   const uint32_t* __restrict__ keys,
                                                                   const uint32_t* __restrict__ events,
-                                                                  const uint8_t* __restrict__ acts, int64_t n,
+                                                                  const uint8_t* __restrict__ acts, int64_t n, int64_t win,
                                                                   int64_t vocab, int n_actions, int d,
                                                                   float* __restrict__ first, float* __restrict__ last,
+                                                                  uint32_t* __restrict__ first_key,
+                                                                  uint32_t* __restrict__ open_key,
                                                                   float* __restrict__ d_item,
                                                                   float* __restrict__ action_part) {
-  extern __shared__ float4 table[];                  // [kSumWarps][n_actions][32]
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float4* mine = table + warp * n_actions * 32;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int64_t windows = (n + kWin - 1) / kWin, stride = (int64_t)gridDim.x * kSumWarps;
-  for (int c0 = 0; c0 < d; c0 += 128) {
-    const int c = c0 + lane * 4;
+  extern __shared__ float4 tables[];                 // [kHalves][n_actions][32]
+  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
+  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+  const Table table{tables + half * n_actions * 32};
+  const int64_t w = (int64_t)blockIdx.x * kHalves + half, p0 = w * win, p1 = min(p0 + win, n);
+  for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
+    const int c = c0 + l * kCols;
     const bool in = c < d;
-    if (kActions)
-      for (int a = 0; a < n_actions; ++a) mine[a * 32 + lane] = zero;
-    for (int64_t w = (int64_t)blockIdx.x * kSumWarps + warp; w < windows; w += stride) {
-      const int64_t p0 = w * kWin;
-      float4 acc = zero;
-      uint32_t run = p0 > 0 ? keys[p0 - 1] : 0xFFFFFFFFu;      // key of the run that acc belongs to
-      bool inside = false;                                      // a head was seen: acc starts at it
-      for (int b = 0; b < kWin && p0 + b < n; b += 32) {
-        const int cnt = (int)min((int64_t)32, n - p0 - b);
-        const uint32_t key = lane < cnt ? keys[p0 + b + lane] : 0xFFFFFFFFu;
-        const uint32_t ev = lane < cnt ? events[p0 + b + lane] : 0u;
-        int act = 0;
-        if (kActions && lane < cnt && key < (uint32_t)vocab) act = acts[ev];
-        for (int j = 0; j < cnt; j += 8) {
-          float4 x[8];
+    if (kActions) table.clear(n_actions, l);
+    if (p0 < p1) {
+      Cols acc = zero_cols();
+      uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;  // key of the run that acc belongs to
+      const uint32_t behind = p1 < n ? keys[p1] : kNone;
+      bool inside = false;                           // a head was seen: acc starts at it
+      uint32_t key_n = p0 + l < p1 ? keys[p0 + l] : kNone, ev_n = p0 + l < p1 ? events[p0 + l] : 0u;
+      if (l == 0 && c0 == 0) first_key[w] = key_n;
+      for (int64_t b = p0; b < p1; b += 16) {
+        const int cnt = (int)min((int64_t)16, p1 - b);
+        const uint32_t key = key_n, ev = ev_n;
+        if (b + 16 + l < p1) {                       // the next 16 positions, a step ahead
+          key_n = keys[b + 16 + l];
+          ev_n = events[b + 16 + l];
+        }
+        int act = -1;
+        if (kActions && l < cnt && key < (uint32_t)vocab) act = acts[ev];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t e = __shfl_sync(0xffffffffu, ev, j + q);
-            x[q] = j + q < cnt && in ? row4(dX + (int64_t)e * d + c) : zero;
+        for (int j = 0; j < 16; j += kBatch) {
+          if (j >= cnt) break;
+          decltype(load_raw(dX)) x[kBatch];
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            const uint32_t e = __shfl_sync(mask, ev, j + q, 16);
+            if (j + q < cnt && in) x[q] = load_raw(dX + (int64_t)e * d + c);
           }
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            if (j + q >= cnt) break;
-            const uint32_t kq = __shfl_sync(0xffffffffu, key, j + q);
-            if (kq != run) {                                    // the same for the whole warp
-              if (in) {
-                if (!inside) *(float4*)(first + w * d + c) = acc;
-                else if (run < (uint32_t)vocab) *(float4*)(d_item + (int64_t)run * d + c) = acc;
+          for (int q = 0; q < kBatch; ++q) {
+            const uint32_t kq = __shfl_sync(mask, key, j + q, 16);
+            const int aq = kActions ? __shfl_sync(mask, act, j + q, 16) : -1;
+            if (j + q < cnt) {                       // the same for the whole half-warp
+              if (kq != run) {
+                if (in) {
+                  if (!inside) store_cols(first + w * d + c, acc);
+                  else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+                }
+                inside = true;
+                run = kq;
+                acc = zero_cols();
               }
-              inside = true;
-              run = kq;
-              acc = zero;
-            }
-            add4(acc, x[q]);
-            if (kActions) {
-              const int aq = __shfl_sync(0xffffffffu, act, j + q);
-              if (kq < (uint32_t)vocab) add4(mine[aq * 32 + lane], x[q]);
+              if (in) {
+                const Cols v = widen(x[q]);
+                add_cols(acc, v);
+                if (kActions && aq >= 0) table.add(aq, l, v);
+              }
             }
           }
         }
       }
-      const bool on = p0 + kWin < n && keys[p0 + kWin] == run;  // the run goes on in the next window
+      const bool on = behind == run;                 // the run goes on in the next window
       if (in) {
-        if (!inside) *(float4*)(first + w * d + c) = acc;
-        else if (on) *(float4*)(last + w * d + c) = acc;
-        else if (run < (uint32_t)vocab) *(float4*)(d_item + (int64_t)run * d + c) = acc;
+        if (!inside) store_cols(first + w * d + c, acc);
+        else if (on) store_cols(last + w * d + c, acc);
+        else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
       }
+      if (l == 0 && c0 == 0) open_key[w] = inside && on && run < (uint32_t)vocab ? run : kNone;
     }
     if (kActions) {
       __syncthreads();
-      for (int e = threadIdx.x; e < n_actions * 32; e += kSumThreads) {
-        const int col = c0 + (e % 32) * 4;
-        float4 acc = table[e];
-        for (int w = 1; w < kSumWarps; ++w) add4(acc, table[w * n_actions * 32 + e]);
-        if (col < d) *(float4*)(action_part + ((int64_t)blockIdx.x * n_actions + e / 32) * d + col) = acc;
-      }
+      store_tables(tables, kHalves, n_actions, c0, d, action_part + (int64_t)blockIdx.x * n_actions * d);
       __syncthreads();
     }
   }
 }
 
-// sum of rows [b, e) of part [., d] at columns c..c+3, in order
-__device__ __forceinline__ float4 sum_range(const float* __restrict__ part, int64_t b, int64_t e, int64_t pitch, bool in) {
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int64_t v = b; v < e; ++v)
-    if (in) add4(acc, *(const float4*)(part + v * pitch));
+// sum of rows [b, e) of a [., pitch] array at 8 columns, in order
+__device__ __forceinline__ Cols sum_range(const float* __restrict__ part, int64_t b, int64_t e, int64_t pitch, bool in) {
+  Cols acc = zero_cols();
+  if (!in) return acc;
+  int64_t v = b;
+  for (; v + kBatch <= e; v += kBatch) {
+    Cols x[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) x[q] = load_cols(part + (v + q) * pitch);
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) add_cols(acc, x[q]);
+  }
+  for (; v < e; ++v) add_cols(acc, load_cols(part + v * pitch));
   return acc;
 }
 
-// the warps' sums added in warp order; the result is in warp 0
-__device__ __forceinline__ float4 sum_warps(float4 mine, float4 (*part)[32]) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+// the half-warps' sums added in order; the result is in half-warp 0
+__device__ __forceinline__ Cols sum_halves(const Cols& mine, Cols (*part)[16]) {
+  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
   __syncthreads();
-  part[warp][lane] = mine;
+  part[half][l] = mine;
   __syncthreads();
-  float4 acc = part[0][lane];
-  for (int w = 1; w < kSumWarps; ++w) add4(acc, part[w][lane]);
+  Cols acc = part[0][l];
+  for (int h = 1; h < kHalves; ++h) add_cols(acc, part[h][l]);
   return acc;
 }
 
-// CTAs [0, window_ctas): a warp per window whose last run started in it and goes on: the run's sum
-// is last[w] + first[w + 1] + ... up to the window where it ends.  Runs over more than kLong
-// windows are added by the whole CTA.  The other CTAs: the action sums, one action each.
-__global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32_t* __restrict__ keys, int64_t n,
-                                                                    int64_t vocab, int d,
+// CTAs [0, action_ctas): the action sums, one action each, from `parts` CTAs' tables.  The others: a
+// half-warp per window whose last run goes on: the run's sum is last[w] + first[w + 1] + ... up to
+// the window where it ends.  Runs over more than kLong windows are added by the whole CTA.
+__global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32_t* __restrict__ first_key,
+                                                                    const uint32_t* __restrict__ open_key,
+                                                                    int64_t windows, int d,
                                                                     const float* __restrict__ first,
                                                                     const float* __restrict__ last,
-                                                                    float* __restrict__ d_item, int window_ctas,
+                                                                    float* __restrict__ d_item, int action_ctas,
                                                                     const float* __restrict__ action_part, int parts,
-                                                                    int n_actions, float* __restrict__ d_action) {
-  __shared__ float4 part[kSumWarps][32];
-  __shared__ int64_t long_end[kSumWarps];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if ((int)blockIdx.x >= window_ctas) {
-    const int a = (int)blockIdx.x - window_ctas;
-    for (int c0 = 0; c0 < d; c0 += 128) {
-      const int c = c0 + lane * 4;
-      const float* p = action_part + (int64_t)a * d + c;
-      const float4 acc = sum_warps(sum_range(p, (int64_t)parts * warp / kSumWarps, (int64_t)parts * (warp + 1) / kSumWarps,
-                                             (int64_t)n_actions * d, c < d), part);
-      if (warp == 0 && c < d) *(float4*)(d_action + (int64_t)a * d + c) = acc;
+                                                                    float* __restrict__ d_action) {
+  __shared__ Cols part[kHalves][16];
+  __shared__ int64_t long_end[kHalves];
+  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
+  if ((int)blockIdx.x < action_ctas) {
+    const int a = (int)blockIdx.x;
+    for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
+      const int c = c0 + l * kCols;
+      const Cols acc = sum_halves(sum_range(action_part + (int64_t)a * d + c, (int64_t)parts * half / kHalves,
+                                            (int64_t)parts * (half + 1) / kHalves, (int64_t)action_ctas * d, c < d), part);
+      if (half == 0 && c < d) store_cols(d_action + (int64_t)a * d + c, acc);
     }
     return;
   }
-  const int64_t w = (int64_t)blockIdx.x * kSumWarps + warp, windows = (n + kWin - 1) / kWin;
+  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+  const int64_t w0 = (int64_t)(blockIdx.x - action_ctas) * kHalves, w = w0 + half;
+  const uint32_t run = w + 1 < windows ? open_key[w] : kNone;
   int64_t end = 0;                                   // one behind the last window of the run (0: none to add)
-  uint32_t run = 0xFFFFFFFFu;
-  if (w + 1 < windows) {
-    run = keys[w * kWin + kWin - 1];
-    if (run < (uint32_t)vocab && keys[(w + 1) * kWin] == run && (w == 0 || keys[w * kWin - 1] != run)) {
-      // window v > w holds a part of the run iff its first key is the run's
-      const int64_t v = w + 1 + lane;
-      const unsigned more = __ballot_sync(0xffffffffu, v < windows && keys[v * kWin] == run);
-      end = w + 1 + __popc(more);
-      if (more == 0xffffffffu) {                     // kLong = 32 windows or more: find the end
-        int64_t lo = w + 33, hi = windows;           // the first window at or behind lo that does not start with it
-        while (lo < hi) {
-          const int64_t mid = (lo + hi) >> 1;
-          if (keys[mid * kWin] == run) lo = mid + 1; else hi = mid;
-        }
-        end = lo;
+  if (run != kNone) {
+    // window v > w holds a part of the run iff its first key is the run's
+    end = w + 1;
+    for (int i = 0; i < kLong; i += 16) {
+      const int64_t v = end + l;
+      const int more = __popc(__ballot_sync(mask, v < windows && first_key[v] == run) & mask);
+      end += more;
+      if (more < 16) break;
+    }
+    if (end == w + 1 + kLong) {                      // find the end, 16 probes at a time
+      int64_t lo = end, hi = windows;                // all windows before lo start with the run, hi does not
+      while (lo < hi) {
+        const int64_t step = (hi - lo + 15) / 16, v = lo + l * step;
+        const int more = __popc(__ballot_sync(mask, v < hi && first_key[v] == run) & mask);
+        if (more == 0) break;
+        hi = min(hi, lo + more * step);
+        lo = lo + (more - 1) * step + 1;
       }
+      end = lo;
     }
   }
   const bool is_long = end - w - 1 >= kLong;
-  if (lane == 0) long_end[warp] = is_long ? end : 0;
+  if (l == 0) long_end[half] = is_long ? end : 0;
   if (end > 0 && !is_long)
-    for (int c = lane * 4; c < d; c += 128) {
-      float4 acc = *(const float4*)(last + w * d + c);
-      add4(acc, sum_range(first + c, w + 1, end, d, true));
-      *(float4*)(d_item + (int64_t)run * d + c) = acc;
+    for (int c = l * kCols; c < d; c += 16 * kCols) {
+      Cols acc = load_cols(last + w * d + c);
+      add_cols(acc, sum_range(first + c, w + 1, end, d, true));
+      store_cols(d_item + (int64_t)run * d + c, acc);
     }
   __syncthreads();
-  for (int i = 0; i < kSumWarps; ++i) {
-    const int64_t e = long_end[i], b = (int64_t)blockIdx.x * kSumWarps + i;
+  for (int i = 0; i < kHalves; ++i) {
+    const int64_t e = long_end[i], b = w0 + i;
     if (e == 0) continue;
     const int64_t cnt = e - b - 1;
-    const uint32_t key = keys[b * kWin + kWin - 1];
-    for (int c0 = 0; c0 < d; c0 += 128) {
-      const int c = c0 + lane * 4;
-      float4 acc = sum_range(first + c, b + 1 + cnt * warp / kSumWarps, b + 1 + cnt * (warp + 1) / kSumWarps, d, c < d);
-      if (warp == 0 && c < d) add4(acc, *(const float4*)(last + b * d + c));
-      acc = sum_warps(acc, part);
-      if (warp == 0 && c < d) *(float4*)(d_item + (int64_t)key * d + c) = acc;
+    const uint32_t key = open_key[b];
+    for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
+      const int c = c0 + l * kCols;
+      Cols acc = sum_range(first + c, b + 1 + cnt * half / kHalves, b + 1 + cnt * (half + 1) / kHalves, d, c < d);
+      if (half == 0 && c < d) add_cols(acc, load_cols(last + b * d + c));
+      acc = sum_halves(acc, part);
+      if (half == 0 && c < d) store_cols(d_item + (int64_t)key * d + c, acc);
     }
   }
 }
 
-// part[CTA][action][d]: the sums of the CTA's contiguous events by action.  Each warp adds its
-// own contiguous part into its own table in shared memory; the warps' tables are added in order.
+// part[CTA][action][d]: the sums of the CTA's contiguous events by action (more actions than the
+// window kernel's tables, or the action gradient alone).  Each half-warp adds its own contiguous
+// part into its own table in shared memory; the tables are added in order.
 template <class T>
 __global__ void action_rows_kernel(const T* __restrict__ dX, const int32_t* __restrict__ ids,
                                    const uint8_t* __restrict__ acts, int64_t n, int64_t per, int64_t vocab,
                                    int n_actions, int d, float* __restrict__ part, int* err) {
-  extern __shared__ float4 table[];                  // [warps][n_actions][32]
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  const int c = blockIdx.y * 128 + lane * 4;
-  float4* mine = table + warp * n_actions * 32;
-  for (int a = 0; a < n_actions; ++a) mine[a * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-  __syncwarp();
+  extern __shared__ float4 tables[];                 // [halves][n_actions][32]
+  const int half = threadIdx.x / 16, l = threadIdx.x % 16, halves = blockDim.x / 16;
+  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+  const int c = blockIdx.y * 16 * kCols + l * kCols;
+  const bool in = c < d;
+  const Table table{tables + half * n_actions * 32};
+  table.clear(n_actions, l);
   const int64_t begin = min((int64_t)blockIdx.x * per, n), end = min(begin + per, n);
-  const int64_t size = (end - begin + warps - 1) / warps;
-  const int64_t wb = min(begin + warp * size, end), we = min(wb + size, end);
+  const int64_t size = (end - begin + halves - 1) / halves;
+  const int64_t wb = min(begin + half * size, end), we = min(wb + size, end);
   bool bad = false;
-  for (int64_t i0 = wb; i0 < we; i0 += 32) {
-    const int cnt = (int)min((int64_t)32, we - i0);
+  for (int64_t i0 = wb; i0 < we; i0 += 16) {
+    const int cnt = (int)min((int64_t)16, we - i0);
     int a = -1;
-    if (lane < cnt) {
-      const bool ok = event_key(ids, acts, i0 + lane, vocab, n_actions) < (uint64_t)vocab;
-      a = ok ? (int)acts[i0 + lane] : -1;
+    if (l < cnt) {
+      const bool ok = event_key(ids, acts, i0 + l, vocab, n_actions) < (uint64_t)vocab;
+      a = ok ? (int)acts[i0 + l] : -1;
       bad |= !ok;
     }
-    for (int j = 0; j < cnt; j += 8) {
-      float4 x[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        x[q] = j + q < cnt && c < d ? row4(dX + (i0 + j + q) * d + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < 16; j += kBatch) {
+      if (j >= cnt) break;
+      decltype(load_raw(dX)) x[kBatch];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int aq = __shfl_sync(0xffffffffu, a, (j + q) & 31);
-        if (j + q < cnt && aq >= 0) add4(mine[aq * 32 + lane], x[q]);
+      for (int q = 0; q < kBatch; ++q)
+        if (j + q < cnt && in) x[q] = load_raw(dX + (i0 + j + q) * d + c);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int aq = __shfl_sync(mask, a, j + q, 16);
+        if (j + q < cnt && aq >= 0 && in) table.add(aq, l, widen(x[q]));
       }
     }
   }
   if (bad && blockIdx.y == 0) atomicOr(err, DEV_ERR_INDEX);
   __syncthreads();
-  for (int e = threadIdx.x; e < n_actions * 32; e += blockDim.x) {
-    const int col = blockIdx.y * 128 + (e % 32) * 4;
-    float4 acc = table[e];
-    for (int w = 1; w < warps; ++w) add4(acc, table[w * n_actions * 32 + e]);
-    if (col < d) *(float4*)(part + ((int64_t)blockIdx.x * n_actions + e / 32) * d + col) = acc;
-  }
+  store_tables(tables, halves, n_actions, blockIdx.y * 16 * kCols, d, part + (int64_t)blockIdx.x * n_actions * d);
 }
 
 int key_bits(int64_t vocab) {
@@ -491,14 +570,17 @@ int key_bits(int64_t vocab) {
 int sort_ctas(int64_t n) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(device_info().sm_count, (n + 1023) / 1024));
 }
-// warps of an action CTA: their tables (512 bytes per action) fit in 128 KB of shared memory
-int action_warps(int n_actions) { return std::max(1, std::min(8, 256 / n_actions)); }
-int action_ctas(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(4 * device_info().sm_count, (n + 255) / 256)); }
-// CTAs of the window kernel: as many as are resident with their action tables (n_actions 4 KB each)
-int window_ctas(int64_t n, int n_actions) {
-  const int64_t ctas = ((n + kWin - 1) / kWin + kSumWarps - 1) / kSumWarps;
-  const int per_sm = n_actions <= 8 ? 6 : 3;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ctas, (int64_t)per_sm * device_info().sm_count));
+// half-warps of an action CTA: their tables (512 bytes per action) fit in 128 KB of shared memory
+int action_halves(int n_actions) { return std::max(1, std::min(kHalves, 256 / n_actions)); }
+int action_ctas(int64_t n) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(4 * device_info().sm_count, (n + 255) / 256));
+}
+// Windows: one per half-warp of the CTAs that are resident at once (64 registers a thread, a table of
+// n_actions 8 KB per CTA), so that all have the same work.
+int64_t window_size(int64_t n, int n_actions) {
+  const int per_sm = n_actions <= 6 ? 4 : n_actions <= 8 ? 3 : n_actions <= 13 ? 2 : 1;
+  const int64_t halves = (int64_t)per_sm * device_info().sm_count * kHalves;
+  return std::max<int64_t>(kMinWin, (n + halves - 1) / halves);
 }
 
 template <class T>
@@ -508,74 +590,77 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
   static std::mutex mu;
   int* err = device_status_word();
   const bool fused = d_item && d_action && n_actions <= kFusedActions;
-  int parts = fused ? window_ctas(n, n_actions) : action_ctas(n);
+  const int64_t win = window_size(n, fused ? n_actions : 0), windows = (n + win - 1) / win;
+  const int window_ctas = (int)((windows + kHalves - 1) / kHalves);
+  const int parts = fused ? window_ctas : action_ctas(n);
   if (d_action && !fused) {
-    const int warps = action_warps(n_actions);
-    const int smem = warps * n_actions * 512;
-    set_smem_limit_once((const void*)action_rows_kernel<T>, 131072, &done[0], mu);
+    const int halves = action_halves(n_actions);
+    const int smem = halves * n_actions * 512;
+    set_smem_limit_once((const void*)action_rows_kernel<T>, 256 * 512, &done[0], mu);
     SA_TIMED("action_rows_kernel", st,
-             (action_rows_kernel<T><<<dim3(parts, (d + 127) / 128), warps * 32, smem, st>>>(
+             (action_rows_kernel<T><<<dim3(parts, (d + 127) / 128), halves * 16, smem, st>>>(
                  dX, ids, acts, n, (n + parts - 1) / parts, vocab, n_actions, d, w.action_part, err)));
   }
-  const uint32_t* keys = nullptr;
   if (d_item) {
     const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, G = sort_ctas(n);
     const int zero_ctas = 2 * device_info().sm_count;
+    const int64_t pieces = vocab * d / 4;            // of 16 bytes
     const FromEvents from{ids, acts, vocab, n_actions};
     if (n <= kSmallN) {
       const int smem = sort_smem((bits + passes - 1) / passes);
-      set_smem_limit_once((const void*)sort_small_kernel, sort_smem(kMaxBits), &done[3], mu);
-      const ZeroRows z{d_item, nullptr, 0, vocab, d};
-      const unsigned grid = 1 + (unsigned)std::min<int64_t>(zero_ctas, (vocab + 511) / 512);
+      set_smem_limit_once((const void*)sort_small_kernel, sort_smem(kMaxBits), &done[1], mu);
+      const ZeroPart z{(float4*)d_item, pieces};
+      const unsigned grid = 1 + (unsigned)std::min<int64_t>(zero_ctas, (pieces + 4 * kSortThreads - 1) / (4 * kSortThreads));
       const Buffers buf{{w.keys[0], w.keys[1]}, {w.events[0], w.events[1]}};
       SA_TIMED("sort_small_kernel", st,
                (sort_small_kernel<<<grid, kSortThreads, smem, st>>>(from, n, bits, passes, buf, z, err)));
     } else {
-      SA_CUDA(cudaMemsetAsync(w.seen, 0, (size_t)(vocab + 31) / 32 * 4, st));
-      set_smem_limit_once((const void*)sort_place_kernel<FromEvents>, sort_smem(kMaxBits), &done[1], mu);
-      set_smem_limit_once((const void*)sort_place_kernel<FromList>, sort_smem(kMaxBits), &done[2], mu);
+      set_smem_limit_once((const void*)sort_place_kernel<FromEvents>, sort_smem(kMaxBits), &done[2], mu);
+      set_smem_limit_once((const void*)sort_place_kernel<FromList>, sort_smem(kMaxBits), &done[3], mu);
+      const int kernels = 4 * passes;                // a count takes one share of the zeros, a placement three
+      auto zeros = [&](int from_share, int to_share) {
+        const int64_t b = pieces * from_share / kernels, e = pieces * to_share / kernels;
+        return ZeroPart{(float4*)d_item + b, e - b};
+      };
       for (int q = 0; q < passes; ++q) {
         Pass ps;
         ps.shift = bits * q / passes;
         ps.bits = bits * (q + 1) / passes - ps.shift;
         ps.n = n;
         ps.per = (n + G - 1) / G;
-        const int smem = sort_smem(ps.bits);
+        const int smem = sort_smem(ps.bits), grid = G + zero_ctas;
         uint32_t *ko = w.keys[q & 1], *eo = w.events[q & 1];
-        // every pass writes its share of the zero rows
-        const ZeroRows z{d_item, w.seen, vocab * q / passes, vocab * (q + 1) / passes, d};
+        const ZeroPart zc = zeros(4 * q, 4 * q + 1), zp = zeros(4 * q + 1, 4 * q + 4);
         if (q == 0) {
-          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<G, kSortThreads, 0, st>>>(from, ps, w.hist, w.seen, err)));
+          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<grid, kSortThreads, 0, st>>>(from, ps, G, w.hist, zc, err)));
           SA_TIMED("sort_place_kernel", st,
-                   (sort_place_kernel<<<G + zero_ctas, kSortThreads, smem, st>>>(from, ps, G, w.hist, ko, eo, z)));
+                   (sort_place_kernel<<<grid, kSortThreads, smem, st>>>(from, ps, G, w.hist, ko, eo, zp)));
         } else {
           const FromList in{w.keys[(q - 1) & 1], w.events[(q - 1) & 1]};
-          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<G, kSortThreads, 0, st>>>(in, ps, w.hist, nullptr, err)));
+          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<grid, kSortThreads, 0, st>>>(in, ps, G, w.hist, zc, err)));
           SA_TIMED("sort_place_kernel", st,
-                   (sort_place_kernel<<<G + zero_ctas, kSortThreads, smem, st>>>(in, ps, G, w.hist, ko, eo, z)));
+                   (sort_place_kernel<<<grid, kSortThreads, smem, st>>>(in, ps, G, w.hist, ko, eo, zp)));
         }
       }
     }
-    keys = w.keys[(passes - 1) & 1];
-    const uint32_t* events = w.events[(passes - 1) & 1];
-    const int ctas = window_ctas(n, fused ? n_actions : 0);
+    const uint32_t *keys = w.keys[(passes - 1) & 1], *events = w.events[(passes - 1) & 1];
     if (fused) {
-      const int smem = kSumWarps * n_actions * 512;
-      set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done[4], mu);
+      const int smem = kHalves * n_actions * 512;
+      set_smem_limit_once((const void*)window_rows_kernel<T, true>, kHalves * kFusedActions * 512, &done[4], mu);
       SA_TIMED("window_rows_kernel", st,
-               (window_rows_kernel<T, true><<<ctas, kSumThreads, smem, st>>>(
-                   dX, keys, events, acts, n, vocab, n_actions, d, w.first, w.last, d_item, w.action_part)));
+               (window_rows_kernel<T, true><<<window_ctas, kSumThreads, smem, st>>>(
+                   dX, keys, events, acts, n, win, vocab, n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item,
+                   w.action_part)));
     } else {
       SA_TIMED("window_rows_kernel", st,
-               (window_rows_kernel<T, false><<<ctas, kSumThreads, 0, st>>>(dX, keys, events, acts, n, vocab, 0, d, w.first,
-                                                                            w.last, d_item, nullptr)));
+               (window_rows_kernel<T, false><<<window_ctas, kSumThreads, 0, st>>>(
+                   dX, keys, events, acts, n, win, vocab, 0, d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr)));
     }
   }
-  const int64_t windows = d_item ? (n + kWin - 1) / kWin : 0;
-  const int wc = (int)((windows + kSumWarps - 1) / kSumWarps);
+  const int ac = d_action ? n_actions : 0;
   SA_TIMED("crossing_rows_kernel", st,
-           (crossing_rows_kernel<<<wc + (d_action ? n_actions : 0), kSumThreads, 0, st>>>(
-               keys, n, vocab, d, w.first, w.last, d_item, wc, w.action_part, parts, n_actions, d_action)));
+           (crossing_rows_kernel<<<ac + (d_item ? window_ctas : 0), kSumThreads, 0, st>>>(
+               w.first_key, w.open_key, windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action)));
   return SA_OK;
 }
 }  // namespace
@@ -583,16 +668,21 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
 size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, int d, EventsBwdWork* w) {
   Carve c(base);
   EventsBwdWork v;
-  const size_t rows = (size_t)std::max<int64_t>(n, 1), windows = (rows + kWin - 1) / kWin;
+  (void)vocab;
+  const size_t rows = (size_t)std::max<int64_t>(n, 1);
+  // the window kernel runs with the action tables or without them
+  const int64_t win = std::min(window_size(n, n_actions), window_size(n, 0));
+  const size_t windows = (size_t)std::max<int64_t>((n + win - 1) / win, 1);
   for (int i = 0; i < 2; ++i) {
     v.keys[i] = c.take<uint32_t>(rows);
     v.events[i] = c.take<uint32_t>(rows);
   }
   v.hist = c.take<int>((size_t)sort_ctas(n) << kMaxBits);
-  v.seen = c.take<unsigned>((size_t)(vocab + 31) / 32);
   v.first = c.take<float>(windows * d);
   v.last = c.take<float>(windows * d);
-  v.action_part = c.take<float>((size_t)std::max(action_ctas(n), window_ctas(n, n_actions)) * n_actions * d);
+  v.first_key = c.take<uint32_t>(windows);
+  v.open_key = c.take<uint32_t>(windows);
+  v.action_part = c.take<float>(std::max((size_t)action_ctas(n), (windows + kHalves - 1) / kHalves) * n_actions * d);
   if (w) *w = v;
   return c.bytes();
 }

@@ -151,8 +151,8 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
 struct EventsBwdWork {
   uint32_t *keys[2], *events[2];   // [n] sorted item ids and their events, in two buffers
   int* hist;             // [sort CTAs, 1024] digit counts
-  unsigned* seen;        // a bit per item: it has events
-  float *first, *last;   // [n / 64, d] sums of the runs that cross a window's begin and end
+  float *first, *last;   // [windows, d] sums of the runs that cross a window's begin and end
+  uint32_t *first_key, *open_key;   // [windows] its first item, and the item whose run goes on behind it
   float* action_part;    // [CTAs, n_actions, d]
 };
 size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, int d, EventsBwdWork* w);

@@ -13,12 +13,13 @@
 // second kernel adds those.  So every row of dX is read once and every half-warp has
 // the same work however popular an item is (under Zipf(1.1) ids over a million items
 // one item has 1 event in 8).  The same pass adds each row to its action's sum, in a
-// table per half-warp in shared memory.
+// table per warp in shared memory.
 //
-// Bound by memory: dX read once, the item gradient written once.  Most of it is zero
-// rows (a million items, 680K events): extra CTAs of the sort's kernels, which by
-// themselves wait on latency and leave the memory idle, zero the whole table (512 MB
-// under 60 us of sorting); the rows with events are written over that.
+// Bound by memory: dX read once, the item gradient written once.  The sort is one
+// cooperative launch (its CTAs exchange digit counts through memory between the passes'
+// steps): half of each CTA's warps sort, which waits on latency and leaves the memory
+// idle, and the other half zero the whole item gradient meanwhile (most of it stays
+// zero: a million items, 680K events); the rows with events are written over that.
 #include <algorithm>
 #include <mutex>
 
@@ -29,19 +30,14 @@ namespace sa {
 
 namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kSmallN = 4096;                // events that one CTA sorts in one launch
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // of a CTA; as many again write zeros
+constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kMinWin = 32;                  // list positions per window, at least
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32, kHalves = 2 * kSumWarps;
 constexpr int kCols = 8;                     // columns per lane: a half-warp covers 128
 constexpr int kBatch = 8;                    // rows in flight per half-warp
 constexpr int kLong = 32;                    // windows of a run that one half-warp adds; longer: the whole CTA
 constexpr int kFusedActions = 16;            // action tables that the window kernel keeps in shared memory
-
-struct Pass {
-  int shift, bits;
-  int64_t n, per;          // events, and events per CTA
-};
 
 // the key of an event: its item id, or `vocab` (behind every item) when the event's id or
 // action is outside its table
@@ -64,122 +60,126 @@ struct FromEvents {
 struct FromList {
   const uint32_t* keys;
   const uint32_t* events;
-  __device__ uint32_t key(int64_t i) const { return keys[i]; }
-  __device__ uint32_t event(int64_t i) const { return events[i]; }
+  // written by other CTAs of this launch: not through L1
+  __device__ uint32_t key(int64_t i) const { return __ldcg(keys + i); }
+  __device__ uint32_t event(int64_t i) const { return __ldcg(events + i); }
   __device__ bool outside(uint32_t) const { return false; }
 };
 
-// `count` 16-byte pieces from `out` on, zeroed by CTA `cta` of `ctas`
-struct ZeroPart {
-  float4* out;
-  int64_t count;
-};
-__device__ __forceinline__ void zero_part(const ZeroPart& z, int cta, int ctas) {
-  const int64_t stride = (int64_t)ctas * blockDim.x;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int64_t i = (int64_t)cta * blockDim.x + threadIdx.x; i < z.count; i += stride) __stcs(z.out + i, zero);
-}
+// barrier of a CTA's sorting warps
+__device__ __forceinline__ void sort_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSortThreads) : "memory"); }
 
-// hist[CTA][bin]: the CTA's events with each digit.  CTAs from `ctas` on zero their part.
-template <class In>
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(In in, Pass ps, int ctas, int* __restrict__ hist,
-                                                                  ZeroPart z, int* err) {
-  __shared__ int cnt[1 << kMaxBits];
-  if ((int)blockIdx.x >= ctas) {
-    zero_part(z, (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
-    return;
-  }
-  const int bins = 1 << ps.bits;
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) cnt[b] = 0;
-  __syncthreads();
-  const int64_t begin = (int64_t)blockIdx.x * ps.per, end = min(begin + ps.per, ps.n);
-  bool bad = false;
-  for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += 4 * kSortThreads) {
-    uint32_t key[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) key[q] = i0 + q * kSortThreads < end ? in.key(i0 + q * kSortThreads) : 0u;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (i0 + q * kSortThreads < end) {
-        bad |= in.outside(key[q]);
-        atomicAdd(&cnt[(key[q] >> ps.shift) & (bins - 1)], 1);
+// Barrier number `round` (from 1) of the sorting CTAs over a counter that starts at zero.  All of
+// them are resident (cooperative launch); the wait is bounded all the same: past the limit it sets
+// the device error word, and the sort goes on over incomplete counts, every index of which is
+// checked before it is used.
+__device__ __forceinline__ void grid_sync(unsigned* counter, unsigned ctas, unsigned round, int* err) {
+  __threadfence();
+  sort_sync();
+  if (threadIdx.x == 0) {
+    atomicAdd(counter, 1u);
+    const long long t0 = clock64();
+    while (*(volatile unsigned*)counter < ctas * round)
+      if (clock64() - t0 > 4000000000LL) {
+        atomicOr(err, DEV_ERR_TIMEOUT);
+        break;
       }
+    __threadfence();
   }
-  if (bad) atomicOr(err, DEV_ERR_INDEX);
-  __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += kSortThreads) hist[(int64_t)blockIdx.x * bins + b] = cnt[b];
+  sort_sync();
 }
 
-// Shared memory of a sorting CTA: wcnt [kSortWarps][bins], base [bins], half [2][bins]
-struct SortSmem {
-  int *wcnt, *base, *half;
-  __device__ SortSmem(int* smem, int bins) : wcnt(smem), base(smem + kSortWarps * bins), half(base + bins) {}
+struct SortArgs {
+  FromEvents in;
+  int64_t n, per;            // events, and events per sorting CTA
+  int bits, passes, ctas;    // of the keys; sorting CTAs
+  uint32_t *keys[2], *events[2];   // the list after pass q is in buffer q & 1
+  int* hist;                 // [ctas][bins] digit counts of a pass, one array per pass parity
+  unsigned* counter;
+  float4* zero;              // the item gradient, and its 16-byte pieces
+  int64_t zeros;
+  int* err;
 };
 constexpr int sort_smem(int bits) { return (kSortWarps + 3) * (1 << bits) * 4; }
 
-// Moves the CTA's events [begin, end) to their places in (keys, events): behind those with smaller
-// digits, and those with the same digit in earlier CTAs (hist, `ctas` of them; NULL: there is one
-// CTA).  Each warp owns a contiguous part, counts its digits, and places its events in order, so
-// equal digits keep their order.
+// One pass over the digit at `shift`: moves the CTA's events behind those with smaller digits, and
+// those with the same digit in earlier CTAs.  Each warp owns a contiguous part, counts its digits,
+// and places its events in order, so equal digits keep their order.
 template <class In>
-__device__ void place(const In& in, const Pass& ps, int cta, int ctas, const int* __restrict__ hist, int* smem,
-                      uint32_t* __restrict__ keys, uint32_t* __restrict__ events) {
+__device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int bits, int* smem, unsigned& round) {
   __shared__ int warp_sum[kSortWarps];
-  const int bins = 1 << ps.bits;
-  const SortSmem sm(smem, bins);
+  const int bins = 1 << bits, cta = blockIdx.x;
+  int *wcnt = smem, *base = smem + kSortWarps * bins, *half = base + bins;   // [warps][bins], [bins], [2][bins]
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int b = threadIdx.x; b < kSortWarps * bins; b += kSortThreads) sm.wcnt[b] = 0;
-  __syncthreads();
-  const int64_t begin = (int64_t)cta * ps.per, end = min(begin + ps.per, ps.n);
+  for (int b = threadIdx.x; b < kSortWarps * bins; b += kSortThreads) wcnt[b] = 0;
+  sort_sync();
+  const int64_t begin = min((int64_t)cta * s.per, s.n), end = min(begin + s.per, s.n);
   const int64_t size = ((end - begin + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const int64_t wb = min(begin + warp * size, end), we = min(wb + size, end);
-  int* mine = sm.wcnt + warp * bins;
-  for (int64_t i = wb + lane; i < we; i += 32) atomicAdd(&mine[(in.key(i) >> ps.shift) & (bins - 1)], 1);
+  int* mine = wcnt + warp * bins;
+  bool bad = false;
+  for (int64_t i0 = wb + lane; i0 < we; i0 += 128) {
+    uint32_t key[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) key[x] = i0 + 32 * x < we ? in.key(i0 + 32 * x) : 0u;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (i0 + 32 * x < we) {
+        bad |= in.outside(key[x]);
+        atomicAdd(&mine[(key[x] >> shift) & (bins - 1)], 1);
+      }
+  }
+  if (bad) atomicOr(s.err, DEV_ERR_INDEX);
+  sort_sync();
   // half[h][b]: events with digit b of the CTAs g = h mod 2; base[b]: of the earlier CTAs
-  if (hist) {
+  int* hist = s.hist + (int64_t)(q & 1) * s.ctas * (1 << kMaxBits);
+  for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) total += wcnt[w * bins + b];
+    if (s.ctas > 1) {
+      hist[(int64_t)cta * bins + b] = total;
+    } else {
+      base[b] = 0;
+      half[b] = total;
+      half[bins + b] = 0;
+    }
+  }
+  if (s.ctas > 1) {
+    grid_sync(s.counter, s.ctas, ++round, s.err);
     // two halves of the CTAs, four bins per thread (bins >= 4)
-    const int quads = bins / 4, q = threadIdx.x % quads, h = threadIdx.x / quads;
+    const int quads = bins / 4, x = threadIdx.x % quads, h = threadIdx.x / quads;
     int4 total = make_int4(0, 0, 0, 0), before = make_int4(0, 0, 0, 0);
     if (h < 2) {
 #pragma unroll 16
-      for (int g = h; g < ctas; g += 2) {
-        const int4 c = *(const int4*)(hist + (int64_t)g * bins + 4 * q);
+      for (int g = h; g < s.ctas; g += 2) {
+        const int4 c = __ldcg((const int4*)(hist + (int64_t)g * bins + 4 * x));
         total.x += c.x; total.y += c.y; total.z += c.z; total.w += c.w;
         if (g < cta) { before.x += c.x; before.y += c.y; before.z += c.z; before.w += c.w; }
       }
-      *(int4*)(sm.half + h * bins + 4 * q) = total;
-      if (h == 0) *(int4*)(sm.base + 4 * q) = before;
+      *(int4*)(half + h * bins + 4 * x) = total;
+      if (h == 0) *(int4*)(base + 4 * x) = before;
     }
-    __syncthreads();
+    sort_sync();
     if (h == 1) {
-      int4 o = *(int4*)(sm.base + 4 * q);
+      int4 o = *(int4*)(base + 4 * x);
       o.x += before.x; o.y += before.y; o.z += before.z; o.w += before.w;
-      *(int4*)(sm.base + 4 * q) = o;
-    }
-  } else {
-    __syncthreads();
-    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
-      int total = 0;
-      for (int w = 0; w < kSortWarps; ++w) total += sm.wcnt[w * bins + b];
-      sm.base[b] = 0;
-      sm.half[b] = total;
-      sm.half[bins + b] = 0;
+      *(int4*)(base + 4 * x) = o;
     }
   }
-  __syncthreads();
+  sort_sync();
   // each warp's first place for each digit
   int carry = 0;
   for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
     const int b = b0 + threadIdx.x;
-    const int total = b < bins ? sm.half[b] + sm.half[bins + b] : 0;
+    const int total = b < bins ? half[b] + half[bins + b] : 0;
     int incl = total;
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
     if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
+    sort_sync();
     int off = carry, all = carry;
     for (int w = 0; w < kSortWarps; ++w) {
       if (w < warp) off += warp_sum[w];
@@ -187,70 +187,55 @@ __device__ void place(const In& in, const Pass& ps, int cta, int ctas, const int
     }
     carry = all;
     if (b < bins) {
-      int run = off + incl - total + sm.base[b];
+      int run = off + incl - total + base[b];
 #pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const int c = sm.wcnt[w * bins + b];
-        sm.wcnt[w * bins + b] = run;
+        const int c = wcnt[w * bins + b];
+        wcnt[w * bins + b] = run;
         run += c;
       }
     }
-    __syncthreads();
+    sort_sync();
   }
+  uint32_t *keys = s.keys[q & 1], *events = s.events[q & 1];
   for (int64_t i0 = wb; i0 < we; i0 += 32) {
     const int64_t i = i0 + lane;
     const bool there = i < we;
     const uint32_t key = there ? in.key(i) : 0u;
-    const int digit = there ? (int)((key >> ps.shift) & (bins - 1)) : -1;
+    const int digit = there ? (int)((key >> shift) & (bins - 1)) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, digit);
     const int rank = __popc(same & ((1u << lane) - 1));
     const int at = there ? mine[digit] : 0;
     __syncwarp();
     if (there) {
       if (rank == 0) mine[digit] = at + __popc(same);
-      keys[at + rank] = key;
-      events[at + rank] = in.event(i);
+      if ((unsigned)(at + rank) < (uint64_t)s.n) {
+        keys[at + rank] = key;
+        events[at + rank] = in.event(i);
+      }
     }
     __syncwarp();
   }
+  if (s.ctas > 1 && q + 1 < s.passes) grid_sync(s.counter, s.ctas, ++round, s.err);
+  else sort_sync();
 }
 
-// CTAs [0, ctas) sort, the others zero their part
-template <class In>
-__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(In in, Pass ps, int ctas, const int* __restrict__ hist,
-                                                                  uint32_t* __restrict__ keys,
-                                                                  uint32_t* __restrict__ events, ZeroPart z) {
+__global__ void __launch_bounds__(2 * kSortThreads, 1) sort_events_kernel(SortArgs s) {
   extern __shared__ __align__(16) int smem[];
-  if ((int)blockIdx.x >= ctas) {
-    zero_part(z, (int)blockIdx.x - ctas, (int)gridDim.x - ctas);
+  if (threadIdx.x >= kSortThreads) {
+    const int64_t stride = (int64_t)gridDim.x * kSortThreads;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x - kSortThreads; i < s.zeros; i += stride)
+      __stcs(s.zero + i, zero);
     return;
   }
-  place(in, ps, (int)blockIdx.x, ctas, hist, smem, keys, events);
-}
-
-// All passes of a short list in CTA 0 (into buffer (passes - 1) & 1); the others zero their part
-struct Buffers {
-  uint32_t *keys[2], *events[2];
-};
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(FromEvents in, int64_t n, int bits, int passes,
-                                                                  Buffers buf, ZeroPart z, int* err) {
-  extern __shared__ __align__(16) int smem[];
-  if (blockIdx.x > 0) {
-    zero_part(z, (int)blockIdx.x - 1, (int)gridDim.x - 1);
-    return;
-  }
-  for (int64_t i = threadIdx.x; i < n; i += kSortThreads)
-    if (in.outside(in.key(i))) atomicOr(err, DEV_ERR_INDEX);
-  for (int q = 0; q < passes; ++q) {
-    const int shift = bits * q / passes;
-    const Pass ps{shift, bits * (q + 1) / passes - shift, n, n};
-    if (q == 0) {
-      place(in, ps, 0, 1, nullptr, smem, buf.keys[0], buf.events[0]);
-    } else {
-      const FromList from{buf.keys[(q - 1) & 1], buf.events[(q - 1) & 1]};
-      place(from, ps, 0, 1, nullptr, smem, buf.keys[q & 1], buf.events[q & 1]);
-    }
-    __syncthreads();                                 // the next pass reads what every warp wrote
+  if ((int)blockIdx.x >= s.ctas) return;
+  unsigned round = 0;
+  for (int q = 0; q < s.passes; ++q) {
+    const int shift = s.bits * q / s.passes, bits = s.bits * (q + 1) / s.passes - shift;
+    if (q == 0) sort_pass(s.in, s, q, shift, bits, smem, round);
+    else sort_pass(FromList{s.keys[(q - 1) & 1], s.events[(q - 1) & 1]}, s, q, shift, bits, smem, round);
   }
 }
 
@@ -295,12 +280,13 @@ __device__ __forceinline__ void store_cols(float* p, const Cols& c) {
   *((float4*)p + 1) = make_float4(c.x[2].x, c.x[2].y, c.x[3].x, c.x[3].y);
 }
 
-// A half-warp's table of action sums in shared memory: [n_actions][2][16 lanes] float4, so that the
+// A warp's table of action sums in shared memory: [n_actions][2][16 lanes] float4, so that the
 // lanes' 16-byte accesses are consecutive
 struct Table {
   float4* base;
-  __device__ void clear(int n_actions, int l) const {
-    for (int a = 0; a < 2 * n_actions; ++a) base[a * 16 + l] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ void clear(int n_actions) const {
+    for (int a = 0; a < n_actions; ++a) base[a * 32 + threadIdx.x % 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+    __syncwarp();
   }
   __device__ void add(int a, int l, const Cols& c) const {
     float4* p = base + a * 32 + l;
@@ -331,87 +317,89 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 // Window w is list positions [win w, win (w + 1)), a half-warp's.  It walks them row by row: a run
 // that lies inside is written to its table row; the sum before the window's first run head goes to
 // first[w], that of a run which goes on behind the window to last[w].  With kActions every row is
-// also added to the half-warp's table of action sums; the CTA's tables go to
-// action_part[CTA][n_actions][d].
+// also added to the warp's table of action sums, one half-warp after the other (a table per
+// half-warp would halve the CTAs per SM); the CTA's tables go to action_part[CTA][n_actions][d].
 template <class T, bool kActions>
-__global__ void __launch_bounds__(kSumThreads) window_rows_kernel(const T* __restrict__ dX,
-                                                                  const uint32_t* __restrict__ keys,
-                                                                  const uint32_t* __restrict__ events,
-                                                                  const uint8_t* __restrict__ acts, int64_t n, int64_t win,
-                                                                  int64_t vocab, int n_actions, int d,
-                                                                  float* __restrict__ first, float* __restrict__ last,
-                                                                  uint32_t* __restrict__ first_key,
-                                                                  uint32_t* __restrict__ open_key,
-                                                                  float* __restrict__ d_item,
-                                                                  float* __restrict__ action_part) {
-  extern __shared__ float4 tables[];                 // [kHalves][n_actions][32]
+__global__ void __launch_bounds__(kSumThreads, 3) window_rows_kernel(const T* __restrict__ dX,
+                                                                     const uint32_t* __restrict__ keys,
+                                                                     const uint32_t* __restrict__ events,
+                                                                     const uint8_t* __restrict__ acts, int64_t n,
+                                                                     int64_t win, int64_t vocab, int n_actions, int d,
+                                                                     float* __restrict__ first, float* __restrict__ last,
+                                                                     uint32_t* __restrict__ first_key,
+                                                                     uint32_t* __restrict__ open_key,
+                                                                     float* __restrict__ d_item,
+                                                                     float* __restrict__ action_part) {
+  extern __shared__ float4 tables[];                 // [kSumWarps][n_actions][32]
   const int half = threadIdx.x / 16, l = threadIdx.x % 16;
-  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-  const Table table{tables + half * n_actions * 32};
-  const int64_t w = (int64_t)blockIdx.x * kHalves + half, p0 = w * win, p1 = min(p0 + win, n);
+  const Table table{tables + threadIdx.x / 32 * n_actions * 32};
+  const int64_t w = (int64_t)blockIdx.x * kHalves + half, p0 = min(w * win, n), p1 = min(p0 + win, n);
   for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
     const int c = c0 + l * kCols;
     const bool in = c < d;
-    if (kActions) table.clear(n_actions, l);
-    if (p0 < p1) {
-      Cols acc = zero_cols();
-      uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;  // key of the run that acc belongs to
-      const uint32_t behind = p1 < n ? keys[p1] : kNone;
-      bool inside = false;                           // a head was seen: acc starts at it
-      uint32_t key_n = p0 + l < p1 ? keys[p0 + l] : kNone, ev_n = p0 + l < p1 ? events[p0 + l] : 0u;
-      if (l == 0 && c0 == 0) first_key[w] = key_n;
-      for (int64_t b = p0; b < p1; b += 16) {
-        const int cnt = (int)min((int64_t)16, p1 - b);
-        const uint32_t key = key_n, ev = ev_n;
-        if (b + 16 + l < p1) {                       // the next 16 positions, a step ahead
-          key_n = keys[b + 16 + l];
-          ev_n = events[b + 16 + l];
+    if (kActions) table.clear(n_actions);
+    Cols acc = zero_cols();
+    uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;    // key of the run that acc belongs to
+    const uint32_t behind = p1 < n ? keys[p1] : kNone;
+    bool inside = false;                             // a head was seen: acc starts at it
+    // (an event number is below n, unless the sort gave up at a barrier)
+    auto event_at = [&](int64_t i) { const uint32_t e = events[i]; return e < (uint64_t)n ? e : 0u; };
+    uint32_t key_n = p0 + l < p1 ? keys[p0 + l] : kNone, ev_n = p0 + l < p1 ? event_at(p0 + l) : 0u;
+    if (l == 0 && c0 == 0 && p0 < p1) first_key[w] = key_n;
+    // both half-warps take the same steps (win is theirs in common); cnt <= 0: behind the window
+    for (int64_t b = p0; b < p0 + win; b += 16) {
+      const int cnt = (int)min((int64_t)16, p1 - b);
+      const uint32_t key = key_n, ev = ev_n;
+      if (b + 16 + l < p1) {                         // the next 16 positions, a step ahead
+        key_n = keys[b + 16 + l];
+        ev_n = event_at(b + 16 + l);
+      }
+      int act = -1;
+      if (kActions && l < cnt && key < (uint32_t)vocab) act = acts[ev];
+#pragma unroll
+      for (int j = 0; j < 16; j += kBatch) {
+        decltype(load_raw(dX)) x[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const uint32_t e = __shfl_sync(0xffffffffu, ev, j + q, 16);
+          if (j + q < cnt && in) x[q] = load_raw(dX + (int64_t)e * d + c);
         }
-        int act = -1;
-        if (kActions && l < cnt && key < (uint32_t)vocab) act = acts[ev];
 #pragma unroll
-        for (int j = 0; j < 16; j += kBatch) {
-          if (j >= cnt) break;
-          decltype(load_raw(dX)) x[kBatch];
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const uint32_t e = __shfl_sync(mask, ev, j + q, 16);
-            if (j + q < cnt && in) x[q] = load_raw(dX + (int64_t)e * d + c);
-          }
-#pragma unroll
-          for (int q = 0; q < kBatch; ++q) {
-            const uint32_t kq = __shfl_sync(mask, key, j + q, 16);
-            const int aq = kActions ? __shfl_sync(mask, act, j + q, 16) : -1;
-            if (j + q < cnt) {                       // the same for the whole half-warp
-              if (kq != run) {
-                if (in) {
-                  if (!inside) store_cols(first + w * d + c, acc);
-                  else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
-                }
-                inside = true;
-                run = kq;
-                acc = zero_cols();
-              }
-              if (in) {
-                const Cols v = widen(x[q]);
-                add_cols(acc, v);
-                if (kActions && aq >= 0) table.add(aq, l, v);
-              }
+        for (int q = 0; q < kBatch; ++q) {
+          const uint32_t kq = __shfl_sync(0xffffffffu, key, j + q, 16);
+          const int aq = kActions ? __shfl_sync(0xffffffffu, act, j + q, 16) : -1;
+          if (j + q < cnt && in) {                   // the same for the whole half-warp, but for idle lanes
+            if (kq != run) {
+              if (!inside) store_cols(first + w * d + c, acc);
+              else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+              acc = zero_cols();
             }
+            add_cols(acc, widen(x[q]));
+          }
+          if (j + q < cnt && kq != run) {
+            inside = true;
+            run = kq;
+          }
+          if (kActions) {
+            const bool add = aq >= 0 && j + q < cnt && in;
+            if (add && half % 2 == 0) table.add(aq, l, widen(x[q]));
+            __syncwarp();
+            if (add && half % 2 == 1) table.add(aq, l, widen(x[q]));
+            __syncwarp();
           }
         }
       }
-      const bool on = behind == run;                 // the run goes on in the next window
-      if (in) {
-        if (!inside) store_cols(first + w * d + c, acc);
-        else if (on) store_cols(last + w * d + c, acc);
-        else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
-      }
-      if (l == 0 && c0 == 0) open_key[w] = inside && on && run < (uint32_t)vocab ? run : kNone;
     }
+    const bool on = behind == run;                   // the run goes on in the next window
+    if (in && p0 < p1) {
+      if (!inside) store_cols(first + w * d + c, acc);
+      else if (on) store_cols(last + w * d + c, acc);
+      else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+    }
+    if (l == 0 && c0 == 0 && p0 < p1) open_key[w] = inside && on && run < (uint32_t)vocab ? run : kNone;
     if (kActions) {
       __syncthreads();
-      store_tables(tables, kHalves, n_actions, c0, d, action_part + (int64_t)blockIdx.x * n_actions * d);
+      store_tables(tables, kSumWarps, n_actions, c0, d, action_part + (int64_t)blockIdx.x * n_actions * d);
       __syncthreads();
     }
   }
@@ -518,48 +506,50 @@ __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32
 }
 
 // part[CTA][action][d]: the sums of the CTA's contiguous events by action (more actions than the
-// window kernel's tables, or the action gradient alone).  Each half-warp adds its own contiguous
-// part into its own table in shared memory; the tables are added in order.
+// window kernel's tables, or the action gradient alone).  Each warp adds its own contiguous part
+// into its own table in shared memory, two rows at a time, one after the other; the tables are added
+// in order.
 template <class T>
 __global__ void action_rows_kernel(const T* __restrict__ dX, const int32_t* __restrict__ ids,
                                    const uint8_t* __restrict__ acts, int64_t n, int64_t per, int64_t vocab,
                                    int n_actions, int d, float* __restrict__ part, int* err) {
-  extern __shared__ float4 tables[];                 // [halves][n_actions][32]
-  const int half = threadIdx.x / 16, l = threadIdx.x % 16, halves = blockDim.x / 16;
-  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+  extern __shared__ float4 tables[];                 // [warps][n_actions][32]
+  const int warp = threadIdx.x / 32, warps = blockDim.x / 32, lane = threadIdx.x % 32, l = lane % 16, h = lane / 16;
   const int c = blockIdx.y * 16 * kCols + l * kCols;
   const bool in = c < d;
-  const Table table{tables + half * n_actions * 32};
-  table.clear(n_actions, l);
+  const Table table{tables + warp * n_actions * 32};
+  table.clear(n_actions);
   const int64_t begin = min((int64_t)blockIdx.x * per, n), end = min(begin + per, n);
-  const int64_t size = (end - begin + halves - 1) / halves;
-  const int64_t wb = min(begin + half * size, end), we = min(wb + size, end);
+  const int64_t size = (end - begin + warps - 1) / warps;
+  const int64_t wb = min(begin + warp * size, end), we = min(wb + size, end);
   bool bad = false;
-  for (int64_t i0 = wb; i0 < we; i0 += 16) {
-    const int cnt = (int)min((int64_t)16, we - i0);
+  for (int64_t i0 = wb; i0 < we; i0 += 32) {
+    const int cnt = (int)min((int64_t)32, we - i0);
     int a = -1;
-    if (l < cnt) {
-      const bool ok = event_key(ids, acts, i0 + l, vocab, n_actions) < (uint64_t)vocab;
-      a = ok ? (int)acts[i0 + l] : -1;
+    if (lane < cnt) {
+      const bool ok = event_key(ids, acts, i0 + lane, vocab, n_actions) < (uint64_t)vocab;
+      a = ok ? (int)acts[i0 + lane] : -1;
       bad |= !ok;
     }
-#pragma unroll
-    for (int j = 0; j < 16; j += kBatch) {
-      if (j >= cnt) break;
+    for (int j = 0; j < cnt; j += 2 * kBatch) {      // rows j + 2 q + h
       decltype(load_raw(dX)) x[kBatch];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q)
-        if (j + q < cnt && in) x[q] = load_raw(dX + (i0 + j + q) * d + c);
+        if (j + 2 * q + h < cnt && in) x[q] = load_raw(dX + (i0 + j + 2 * q + h) * d + c);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int aq = __shfl_sync(mask, a, j + q, 16);
-        if (j + q < cnt && aq >= 0 && in) table.add(aq, l, widen(x[q]));
+        const int aq = __shfl_sync(0xffffffffu, a, j + 2 * q + h);
+        const bool add = j + 2 * q + h < cnt && aq >= 0 && in;
+        if (add && h == 0) table.add(aq, l, widen(x[q]));
+        __syncwarp();
+        if (add && h == 1) table.add(aq, l, widen(x[q]));
+        __syncwarp();
       }
     }
   }
   if (bad && blockIdx.y == 0) atomicOr(err, DEV_ERR_INDEX);
   __syncthreads();
-  store_tables(tables, halves, n_actions, blockIdx.y * 16 * kCols, d, part + (int64_t)blockIdx.x * n_actions * d);
+  store_tables(tables, warps, n_actions, blockIdx.y * 16 * kCols, d, part + (int64_t)blockIdx.x * n_actions * d);
 }
 
 int key_bits(int64_t vocab) {
@@ -568,85 +558,59 @@ int key_bits(int64_t vocab) {
   return b;
 }
 int sort_ctas(int64_t n) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(device_info().sm_count, (n + 1023) / 1024));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(device_info().sm_count, (n + kSortPer - 1) / kSortPer));
 }
-// half-warps of an action CTA: their tables (512 bytes per action) fit in 128 KB of shared memory
-int action_halves(int n_actions) { return std::max(1, std::min(kHalves, 256 / n_actions)); }
+// warps of an action CTA: their tables (512 bytes per action) fit in 128 KB of shared memory
+int action_warps(int n_actions) { return std::max(1, std::min(kSumWarps, 256 / n_actions)); }
 int action_ctas(int64_t n) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(4 * device_info().sm_count, (n + 255) / 256));
 }
-// Windows: one per half-warp of the CTAs that are resident at once (64 registers a thread, a table of
-// n_actions 8 KB per CTA), so that all have the same work.
-int64_t window_size(int64_t n, int n_actions) {
-  const int per_sm = n_actions <= 6 ? 4 : n_actions <= 8 ? 3 : n_actions <= 13 ? 2 : 1;
-  const int64_t halves = (int64_t)per_sm * device_info().sm_count * kHalves;
+// Windows: one per half-warp of the CTAs that are resident at once (three per SM, their registers'
+// limit: 16 tables take 64 KB of a CTA's shared memory), so that all have the same work.
+int64_t window_size(int64_t n) {
+  const int64_t halves = (int64_t)3 * device_info().sm_count * kHalves;
   return std::max<int64_t>(kMinWin, (n + halves - 1) / halves);
 }
 
 template <class T>
 sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, int64_t vocab, int n_actions, int d,
               float* d_item, float* d_action, const EventsBwdWork& w, cudaStream_t st) {
-  static unsigned long long done[5] = {};          // one per kernel
+  static unsigned long long done[3] = {};          // one per kernel
   static std::mutex mu;
   int* err = device_status_word();
   const bool fused = d_item && d_action && n_actions <= kFusedActions;
-  const int64_t win = window_size(n, fused ? n_actions : 0), windows = (n + win - 1) / win;
+  const int64_t win = window_size(n), windows = (n + win - 1) / win;
   const int window_ctas = (int)((windows + kHalves - 1) / kHalves);
   const int parts = fused ? window_ctas : action_ctas(n);
   if (d_action && !fused) {
-    const int halves = action_halves(n_actions);
-    const int smem = halves * n_actions * 512;
+    const int warps = action_warps(n_actions);
+    const int smem = warps * n_actions * 512;
     set_smem_limit_once((const void*)action_rows_kernel<T>, 256 * 512, &done[0], mu);
     SA_TIMED("action_rows_kernel", st,
-             (action_rows_kernel<T><<<dim3(parts, (d + 127) / 128), halves * 16, smem, st>>>(
+             (action_rows_kernel<T><<<dim3(parts, (d + 127) / 128), warps * 32, smem, st>>>(
                  dX, ids, acts, n, (n + parts - 1) / parts, vocab, n_actions, d, w.action_part, err)));
   }
   if (d_item) {
-    const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits, G = sort_ctas(n);
-    const int zero_ctas = 2 * device_info().sm_count;
-    const int64_t pieces = vocab * d / 4;            // of 16 bytes
-    const FromEvents from{ids, acts, vocab, n_actions};
-    if (n <= kSmallN) {
-      const int smem = sort_smem((bits + passes - 1) / passes);
-      set_smem_limit_once((const void*)sort_small_kernel, sort_smem(kMaxBits), &done[1], mu);
-      const ZeroPart z{(float4*)d_item, pieces};
-      const unsigned grid = 1 + (unsigned)std::min<int64_t>(zero_ctas, (pieces + 4 * kSortThreads - 1) / (4 * kSortThreads));
-      const Buffers buf{{w.keys[0], w.keys[1]}, {w.events[0], w.events[1]}};
-      SA_TIMED("sort_small_kernel", st,
-               (sort_small_kernel<<<grid, kSortThreads, smem, st>>>(from, n, bits, passes, buf, z, err)));
+    const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
+    SortArgs s{{ids, acts, vocab, n_actions}, n, 0, bits, passes, sort_ctas(n), {w.keys[0], w.keys[1]},
+               {w.events[0], w.events[1]}, w.hist, w.counter, (float4*)d_item, vocab * d / 4, err};
+    s.per = (n + s.ctas - 1) / s.ctas;
+    set_smem_limit_once((const void*)sort_events_kernel, sort_smem(kMaxBits), &done[1], mu);
+    const int smem = sort_smem((bits + passes - 1) / passes);
+    if (s.ctas == 1) {
+      SA_TIMED("sort_events_kernel", st,
+               (sort_events_kernel<<<device_info().sm_count, 2 * kSortThreads, smem, st>>>(s)));
     } else {
-      set_smem_limit_once((const void*)sort_place_kernel<FromEvents>, sort_smem(kMaxBits), &done[2], mu);
-      set_smem_limit_once((const void*)sort_place_kernel<FromList>, sort_smem(kMaxBits), &done[3], mu);
-      const int kernels = 4 * passes;                // a count takes one share of the zeros, a placement three
-      auto zeros = [&](int from_share, int to_share) {
-        const int64_t b = pieces * from_share / kernels, e = pieces * to_share / kernels;
-        return ZeroPart{(float4*)d_item + b, e - b};
-      };
-      for (int q = 0; q < passes; ++q) {
-        Pass ps;
-        ps.shift = bits * q / passes;
-        ps.bits = bits * (q + 1) / passes - ps.shift;
-        ps.n = n;
-        ps.per = (n + G - 1) / G;
-        const int smem = sort_smem(ps.bits), grid = G + zero_ctas;
-        uint32_t *ko = w.keys[q & 1], *eo = w.events[q & 1];
-        const ZeroPart zc = zeros(4 * q, 4 * q + 1), zp = zeros(4 * q + 1, 4 * q + 4);
-        if (q == 0) {
-          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<grid, kSortThreads, 0, st>>>(from, ps, G, w.hist, zc, err)));
-          SA_TIMED("sort_place_kernel", st,
-                   (sort_place_kernel<<<grid, kSortThreads, smem, st>>>(from, ps, G, w.hist, ko, eo, zp)));
-        } else {
-          const FromList in{w.keys[(q - 1) & 1], w.events[(q - 1) & 1]};
-          SA_TIMED("sort_count_kernel", st, (sort_count_kernel<<<grid, kSortThreads, 0, st>>>(in, ps, G, w.hist, zc, err)));
-          SA_TIMED("sort_place_kernel", st,
-                   (sort_place_kernel<<<grid, kSortThreads, smem, st>>>(in, ps, G, w.hist, ko, eo, zp)));
-        }
-      }
+      SA_CUDA(cudaMemsetAsync(w.counter, 0, sizeof(unsigned), st));
+      void* args[] = {&s};
+      SA_TIMED("sort_events_kernel", st,
+               cudaLaunchCooperativeKernel((const void*)sort_events_kernel, dim3(device_info().sm_count),
+                                           dim3(2 * kSortThreads), args, (size_t)smem, st));
     }
     const uint32_t *keys = w.keys[(passes - 1) & 1], *events = w.events[(passes - 1) & 1];
     if (fused) {
-      const int smem = kHalves * n_actions * 512;
-      set_smem_limit_once((const void*)window_rows_kernel<T, true>, kHalves * kFusedActions * 512, &done[4], mu);
+      const int smem = kSumWarps * n_actions * 512;
+      set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done[2], mu);
       SA_TIMED("window_rows_kernel", st,
                (window_rows_kernel<T, true><<<window_ctas, kSumThreads, smem, st>>>(
                    dX, keys, events, acts, n, win, vocab, n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item,
@@ -670,14 +634,14 @@ size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, in
   EventsBwdWork v;
   (void)vocab;
   const size_t rows = (size_t)std::max<int64_t>(n, 1);
-  // the window kernel runs with the action tables or without them
-  const int64_t win = std::min(window_size(n, n_actions), window_size(n, 0));
+  const int64_t win = window_size(n);
   const size_t windows = (size_t)std::max<int64_t>((n + win - 1) / win, 1);
   for (int i = 0; i < 2; ++i) {
     v.keys[i] = c.take<uint32_t>(rows);
     v.events[i] = c.take<uint32_t>(rows);
   }
-  v.hist = c.take<int>((size_t)sort_ctas(n) << kMaxBits);
+  v.hist = c.take<int>((size_t)2 * sort_ctas(n) << kMaxBits);
+  v.counter = c.take<unsigned>(1);
   v.first = c.take<float>(windows * d);
   v.last = c.take<float>(windows * d);
   v.first_key = c.take<uint32_t>(windows);

@@ -8,9 +8,9 @@
 // The rows are ordered by item id with a stable radix sort of (id, event) pairs (an
 // LSD pass per kMaxBits bits of the vocabulary's size: two for a million items), so
 // every table row's gradient is the sum of a contiguous run of the list, in the order
-// of the events.  The list is cut into equal windows, one per half-warp: runs inside a
+// of the events.  The list is cut into equal windows, one per warp: runs inside a
 // window are written at once, the sums of the runs that cross its ends are kept, and a
-// second kernel adds those.  So every row of dX is read once and every half-warp has
+// second kernel adds those.  So every row of dX is read once and every warp has
 // the same work however popular an item is (under Zipf(1.1) ids over a million items
 // one item has 1 event in 8).  The same pass adds each row to its action's sum, in a
 // table per warp in shared memory.
@@ -32,11 +32,10 @@ namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // of a CTA; as many again write zeros
 constexpr int kSortPer = 1024;               // events per sorting CTA, at least
+constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
-constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32, kHalves = 2 * kSumWarps;
-constexpr int kCols = 8;                     // columns per lane: a half-warp covers 128
-constexpr int kBatch = 8;                    // rows in flight per half-warp
-constexpr int kLong = 32;                    // windows of a run that one half-warp adds; longer: the whole CTA
+constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kWindowCtas = 3;               // window CTAs per SM: 16 tables take 64 KB of shared memory each
 constexpr int kFusedActions = 16;            // action tables that the window kernel keeps in shared memory
 
 // the key of an event: its item id, or `vocab` (behind every item) when the event's id or
@@ -118,17 +117,33 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
   const int64_t wb = min(begin + warp * size, end), we = min(wb + size, end);
   int* mine = wcnt + warp * bins;
   bool bad = false;
-  for (int64_t i0 = wb + lane; i0 < we; i0 += 128) {
-    uint32_t key[4];
+  // the first kHeld keys of each lane stay in registers until they are placed (under the writes of
+  // the zeros a load takes microseconds); longer parts are read again, kHeld at a time
+  uint32_t key[kHeld], ev[kHeld];
+  auto load = [&](int64_t i0) {
 #pragma unroll
-    for (int x = 0; x < 4; ++x) key[x] = i0 + 32 * x < we ? in.key(i0 + 32 * x) : 0u;
+    for (int x = 0; x < kHeld; ++x) {
+      const int64_t i = i0 + 32 * x + lane;
+      key[x] = i < we ? in.key(i) : 0u;
+      ev[x] = i < we ? in.event(i) : 0u;
+    }
+  };
+  for (int64_t i0 = wb + 32 * kHeld; i0 < we; i0 += 32 * kHeld) {
+    load(i0);
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (i0 + 32 * x < we) {
+    for (int x = 0; x < kHeld; ++x)
+      if (i0 + 32 * x + lane < we) {
         bad |= in.outside(key[x]);
         atomicAdd(&mine[(key[x] >> shift) & (bins - 1)], 1);
       }
   }
+  load(wb);
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x)
+    if (wb + 32 * x + lane < we) {
+      bad |= in.outside(key[x]);
+      atomicAdd(&mine[(key[x] >> shift) & (bins - 1)], 1);
+    }
   if (bad) atomicOr(s.err, DEV_ERR_INDEX);
   sort_sync();
   // half[h][b]: events with digit b of the CTAs g = h mod 2; base[b]: of the earlier CTAs
@@ -198,23 +213,26 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
     sort_sync();
   }
   uint32_t *keys = s.keys[q & 1], *events = s.events[q & 1];
-  for (int64_t i0 = wb; i0 < we; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const bool there = i < we;
-    const uint32_t key = there ? in.key(i) : 0u;
-    const int digit = there ? (int)((key >> shift) & (bins - 1)) : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, digit);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    const int at = there ? mine[digit] : 0;
-    __syncwarp();
-    if (there) {
-      if (rank == 0) mine[digit] = at + __popc(same);
-      if ((unsigned)(at + rank) < (uint64_t)s.n) {
-        keys[at + rank] = key;
-        events[at + rank] = in.event(i);
+  for (int64_t i0 = wb; i0 < we; i0 += 32 * kHeld) {
+    if (i0 > wb) load(i0);
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      if (i0 + 32 * x >= we) break;
+      const bool there = i0 + 32 * x + lane < we;
+      const int digit = there ? (int)((key[x] >> shift) & (bins - 1)) : -1;
+      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      const int rank = __popc(same & ((1u << lane) - 1));
+      const int at = there ? mine[digit] : 0;
+      __syncwarp();
+      if (there) {
+        if (rank == 0) mine[digit] = at + __popc(same);
+        if ((unsigned)(at + rank) < (uint64_t)s.n) {
+          keys[at + rank] = key[x];
+          events[at + rank] = ev[x];
+        }
       }
+      __syncwarp();
     }
-    __syncwarp();
   }
   if (s.ctas > 1 && q + 1 < s.passes) grid_sync(s.counter, s.ctas, ++round, s.err);
   else sort_sync();
@@ -239,164 +257,126 @@ __global__ void __launch_bounds__(2 * kSortThreads, 1) sort_events_kernel(SortAr
   }
 }
 
-// 8 columns of a row, as they lie in memory
-struct RawB {
-  uint4 w;
+// 4 columns of a row, as they lie in memory
+__device__ __forceinline__ uint2 load_raw(const __nv_bfloat16* p) { return __ldcs((const uint2*)p); }
+__device__ __forceinline__ float4 load_raw(const float* p) { return __ldcs((const float4*)p); }
+struct Cols {                                // 4 fp32 columns, added in pairs
+  float2 a, b;
 };
-struct RawF {
-  float4 a, b;
-};
-__device__ __forceinline__ RawB load_raw(const __nv_bfloat16* p) { return {__ldcs((const uint4*)p)}; }
-__device__ __forceinline__ RawF load_raw(const float* p) {
-  return {__ldcs((const float4*)p), __ldcs((const float4*)p + 1)};
+__device__ __forceinline__ Cols widen(const uint2& w) {
+  return {make_float2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u)),
+          make_float2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u))};
 }
-struct Cols {                                // 8 fp32 columns, added in pairs
-  float2 x[4];
-};
-__device__ __forceinline__ Cols widen(const RawB& r) {
-  const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-  Cols c;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c.x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-  return c;
+__device__ __forceinline__ Cols widen(const float4& r) { return {make_float2(r.x, r.y), make_float2(r.z, r.w)}; }
+__device__ __forceinline__ Cols zero_cols() { return {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}; }
+__device__ __forceinline__ void add_cols(Cols& x, const Cols& y) {
+  x.a = __fadd2_rn(x.a, y.a);
+  x.b = __fadd2_rn(x.b, y.b);
 }
-__device__ __forceinline__ Cols widen(const RawF& r) {
-  return {{make_float2(r.a.x, r.a.y), make_float2(r.a.z, r.a.w), make_float2(r.b.x, r.b.y), make_float2(r.b.z, r.b.w)}};
-}
-__device__ __forceinline__ Cols zero_cols() {
-  const float2 z = make_float2(0.f, 0.f);
-  return {{z, z, z, z}};
-}
-__device__ __forceinline__ void add_cols(Cols& a, const Cols& b) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a.x[i] = __fadd2_rn(a.x[i], b.x[i]);
-}
-__device__ __forceinline__ Cols load_cols(const float* p) {
-  const float4 a = *(const float4*)p, b = *((const float4*)p + 1);
-  return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
-}
+__device__ __forceinline__ Cols load_cols(const float* p) { return widen(*(const float4*)p); }
 __device__ __forceinline__ void store_cols(float* p, const Cols& c) {
-  *(float4*)p = make_float4(c.x[0].x, c.x[0].y, c.x[1].x, c.x[1].y);
-  *((float4*)p + 1) = make_float4(c.x[2].x, c.x[2].y, c.x[3].x, c.x[3].y);
+  *(float4*)p = make_float4(c.a.x, c.a.y, c.b.x, c.b.y);
 }
+template <class T>
+constexpr int batch_rows() { return sizeof(T) == 2 ? 16 : 8; }   // rows in flight per warp: 32 registers
 
-// A warp's table of action sums in shared memory: [n_actions][2][16 lanes] float4, so that the
-// lanes' 16-byte accesses are consecutive
-struct Table {
-  float4* base;
-  __device__ void clear(int n_actions) const {
-    for (int a = 0; a < n_actions; ++a) base[a * 32 + threadIdx.x % 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncwarp();
-  }
-  __device__ void add(int a, int l, const Cols& c) const {
-    float4* p = base + a * 32 + l;
-    float4 u = p[0], v = p[16];
-    u.x += c.x[0].x; u.y += c.x[0].y; u.z += c.x[1].x; u.w += c.x[1].y;
-    v.x += c.x[2].x; v.y += c.x[2].y; v.z += c.x[3].x; v.w += c.x[3].y;
-    p[0] = u;
-    p[16] = v;
-  }
-};
-// the CTA's tables, added in order, to out[n_actions][d] (columns c0 .. c0 + 127 of it)
+// the CTA's tables of action sums (per warp [n_actions][32 lanes] float4), added in order, to
+// out[n_actions][d] (columns c0 .. c0 + 127 of it)
 __device__ __forceinline__ void store_tables(const float4* tables, int count, int n_actions, int c0, int d, float* out) {
   for (int e = threadIdx.x; e < n_actions * 32; e += blockDim.x) {
-    const int col = c0 + (e % 16) * kCols + (e / 16) % 2 * 4;
-    float4 acc = tables[e];
-    for (int h = 1; h < count; ++h) {
-      const float4 x = tables[h * n_actions * 32 + e];
-      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
-    }
-    if (col < d) *(float4*)(out + (int64_t)(e / 32) * d + col) = acc;
+    const int col = c0 + e % 32 * 4;
+    Cols acc = widen(tables[e]);
+    for (int h = 1; h < count; ++h) add_cols(acc, widen(tables[h * n_actions * 32 + e]));
+    if (col < d) store_cols(out + (int64_t)(e / 32) * d + col, acc);
   }
 }
+__device__ __forceinline__ void add_to_table(float4* row, const Cols& v) {
+  Cols s = widen(*row);
+  add_cols(s, v);
+  *row = make_float4(s.a.x, s.a.y, s.b.x, s.b.y);
+}
 
-// What a window leaves for the second kernel: its first key, and the key of its last run if that
-// starts in it and goes on behind it (else kNone).
-constexpr uint32_t kNone = 0xFFFFFFFFu;
+constexpr uint32_t kNone = 0xFFFFFFFFu;      // no item
 
-// Window w is list positions [win w, win (w + 1)), a half-warp's.  It walks them row by row: a run
-// that lies inside is written to its table row; the sum before the window's first run head goes to
-// first[w], that of a run which goes on behind the window to last[w].  With kActions every row is
-// also added to the warp's table of action sums, one half-warp after the other (a table per
-// half-warp would halve the CTAs per SM); the CTA's tables go to action_part[CTA][n_actions][d].
+// Window w is list positions [win w, win (w + 1)), a warp's.  It walks them row by row: a run that
+// lies inside is written to its table row; the sum before the window's first run head goes to
+// first[w], that of a run which starts in it and goes on behind it to last[w]; first_key[w] and
+// open_key[w] (kNone: no run goes on) tell the second kernel which.  With kActions every row is also
+// added to the warp's table of action sums; the CTA's tables go to action_part[CTA][n_actions][d].
 template <class T, bool kActions>
-__global__ void __launch_bounds__(kSumThreads, 3) window_rows_kernel(const T* __restrict__ dX,
-                                                                     const uint32_t* __restrict__ keys,
-                                                                     const uint32_t* __restrict__ events,
-                                                                     const uint8_t* __restrict__ acts, int64_t n,
-                                                                     int64_t win, int64_t vocab, int n_actions, int d,
-                                                                     float* __restrict__ first, float* __restrict__ last,
-                                                                     uint32_t* __restrict__ first_key,
-                                                                     uint32_t* __restrict__ open_key,
-                                                                     float* __restrict__ d_item,
-                                                                     float* __restrict__ action_part) {
+__global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
+    const T* __restrict__ dX, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ events,
+    const uint8_t* __restrict__ acts, int64_t n, int64_t win, int64_t vocab, int n_actions, int d,
+    float* __restrict__ first, float* __restrict__ last, uint32_t* __restrict__ first_key,
+    uint32_t* __restrict__ open_key, float* __restrict__ d_item, float* __restrict__ action_part) {
   extern __shared__ float4 tables[];                 // [kSumWarps][n_actions][32]
-  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
-  const Table table{tables + threadIdx.x / 32 * n_actions * 32};
-  const int64_t w = (int64_t)blockIdx.x * kHalves + half, p0 = min(w * win, n), p1 = min(p0 + win, n);
-  for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
-    const int c = c0 + l * kCols;
+  constexpr int kBatch = batch_rows<T>();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float4* mine = tables + warp * n_actions * 32 + lane;
+  const int64_t w = (int64_t)blockIdx.x * kSumWarps + warp, p0 = min(w * win, n), p1 = min(p0 + win, n);
+  for (int c0 = 0; c0 < d; c0 += 128) {
+    const int c = c0 + lane * 4;
     const bool in = c < d;
-    if (kActions) table.clear(n_actions);
-    Cols acc = zero_cols();
-    uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;    // key of the run that acc belongs to
-    const uint32_t behind = p1 < n ? keys[p1] : kNone;
-    bool inside = false;                             // a head was seen: acc starts at it
-    // (an event number is below n, unless the sort gave up at a barrier)
-    auto event_at = [&](int64_t i) { const uint32_t e = events[i]; return e < (uint64_t)n ? e : 0u; };
-    uint32_t key_n = p0 + l < p1 ? keys[p0 + l] : kNone, ev_n = p0 + l < p1 ? event_at(p0 + l) : 0u;
-    if (l == 0 && c0 == 0 && p0 < p1) first_key[w] = key_n;
-    // both half-warps take the same steps (win is theirs in common); cnt <= 0: behind the window
-    for (int64_t b = p0; b < p0 + win; b += 16) {
-      const int cnt = (int)min((int64_t)16, p1 - b);
-      const uint32_t key = key_n, ev = ev_n;
-      if (b + 16 + l < p1) {                         // the next 16 positions, a step ahead
-        key_n = keys[b + 16 + l];
-        ev_n = event_at(b + 16 + l);
-      }
-      int act = -1;
-      if (kActions && l < cnt && key < (uint32_t)vocab) act = acts[ev];
-#pragma unroll
-      for (int j = 0; j < 16; j += kBatch) {
-        decltype(load_raw(dX)) x[kBatch];
-#pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const uint32_t e = __shfl_sync(0xffffffffu, ev, j + q, 16);
-          if (j + q < cnt && in) x[q] = load_raw(dX + (int64_t)e * d + c);
+    if (kActions)
+      for (int a = 0; a < n_actions; ++a) mine[a * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p0 < p1) {
+      const T* col = dX + (in ? c : 0);              // idle lanes read (and drop) the first columns
+      Cols acc = zero_cols();
+      uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;  // key of the run that acc belongs to
+      const uint32_t behind = p1 < n ? keys[p1] : kNone;
+      bool inside = false;                           // a head was seen: acc starts at it
+      // (an event number is below n, unless the sort gave up at a barrier)
+      auto event_at = [&](int64_t i) { const uint32_t e = events[i]; return e < (uint64_t)n ? e : 0u; };
+      uint32_t key_n = p0 + lane < p1 ? keys[p0 + lane] : kNone, ev_n = p0 + lane < p1 ? event_at(p0 + lane) : 0u;
+      if (lane == 0 && c0 == 0) first_key[w] = key_n;
+      for (int64_t b = p0; b < p1; b += 32) {
+        const int cnt = (int)min((int64_t)32, p1 - b);
+        const uint32_t key = key_n, ev = ev_n;
+        if (b + 32 + lane < p1) {                    // the next 32 positions, a step ahead
+          key_n = keys[b + 32 + lane];
+          ev_n = event_at(b + 32 + lane);
         }
+        int act = -1;
+        if (kActions && lane < cnt && key < (uint32_t)vocab) act = acts[ev];
+        uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
+        if (lane == 0) prev = run;
+        const unsigned heads = __ballot_sync(0xffffffffu, lane < cnt && key != prev);
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-          const uint32_t kq = __shfl_sync(0xffffffffu, key, j + q, 16);
-          const int aq = kActions ? __shfl_sync(0xffffffffu, act, j + q, 16) : -1;
-          if (j + q < cnt && in) {                   // the same for the whole half-warp, but for idle lanes
-            if (kq != run) {
-              if (!inside) store_cols(first + w * d + c, acc);
-              else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+        for (int j = 0; j < 32; j += kBatch) {
+          if (j >= cnt) break;
+          decltype(load_raw(dX)) x[kBatch];
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q)           // behind the window's end: event 0, dropped
+            x[q] = load_raw(col + (int64_t)__shfl_sync(0xffffffffu, ev, j + q) * d);
+#pragma unroll
+          for (int q = 0; q < kBatch; ++q) {
+            if (j + q >= cnt) break;
+            if ((heads >> (j + q)) & 1) {            // the same for the whole warp
+              if (in) {
+                if (!inside) store_cols(first + w * d + c, acc);
+                else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+              }
+              inside = true;
+              run = __shfl_sync(0xffffffffu, key, j + q);
               acc = zero_cols();
             }
-            add_cols(acc, widen(x[q]));
-          }
-          if (j + q < cnt && kq != run) {
-            inside = true;
-            run = kq;
-          }
-          if (kActions) {
-            const bool add = aq >= 0 && j + q < cnt && in;
-            if (add && half % 2 == 0) table.add(aq, l, widen(x[q]));
-            __syncwarp();
-            if (add && half % 2 == 1) table.add(aq, l, widen(x[q]));
-            __syncwarp();
+            const Cols v = widen(x[q]);
+            add_cols(acc, v);
+            if (kActions) {
+              const int a = __shfl_sync(0xffffffffu, act, j + q);
+              if (a >= 0) add_to_table(mine + a * 32, v);
+            }
           }
         }
       }
+      const bool on = behind == run;                 // the run goes on in the next window
+      if (in) {
+        if (!inside) store_cols(first + w * d + c, acc);
+        else if (on) store_cols(last + w * d + c, acc);
+        else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
+      }
+      if (lane == 0 && c0 == 0) open_key[w] = inside && on && run < (uint32_t)vocab ? run : kNone;
     }
-    const bool on = behind == run;                   // the run goes on in the next window
-    if (in && p0 < p1) {
-      if (!inside) store_cols(first + w * d + c, acc);
-      else if (on) store_cols(last + w * d + c, acc);
-      else if (run < (uint32_t)vocab) store_cols(d_item + (int64_t)run * d + c, acc);
-    }
-    if (l == 0 && c0 == 0 && p0 < p1) open_key[w] = inside && on && run < (uint32_t)vocab ? run : kNone;
     if (kActions) {
       __syncthreads();
       store_tables(tables, kSumWarps, n_actions, c0, d, action_part + (int64_t)blockIdx.x * n_actions * d);
@@ -405,36 +385,36 @@ __global__ void __launch_bounds__(kSumThreads, 3) window_rows_kernel(const T* __
   }
 }
 
-// sum of rows [b, e) of a [., pitch] array at 8 columns, in order
+// sum of rows [b, e) of a [., pitch] array at 4 columns, in order
 __device__ __forceinline__ Cols sum_range(const float* __restrict__ part, int64_t b, int64_t e, int64_t pitch, bool in) {
   Cols acc = zero_cols();
   if (!in) return acc;
   int64_t v = b;
-  for (; v + kBatch <= e; v += kBatch) {
-    Cols x[kBatch];
+  for (; v + 8 <= e; v += 8) {
+    Cols x[8];
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) x[q] = load_cols(part + (v + q) * pitch);
+    for (int q = 0; q < 8; ++q) x[q] = load_cols(part + (v + q) * pitch);
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) add_cols(acc, x[q]);
+    for (int q = 0; q < 8; ++q) add_cols(acc, x[q]);
   }
   for (; v < e; ++v) add_cols(acc, load_cols(part + v * pitch));
   return acc;
 }
 
-// the half-warps' sums added in order; the result is in half-warp 0
-__device__ __forceinline__ Cols sum_halves(const Cols& mine, Cols (*part)[16]) {
-  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
+// the warps' sums added in order; the result is in warp 0
+__device__ __forceinline__ Cols sum_warps(const Cols& mine, Cols (*part)[32]) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   __syncthreads();
-  part[half][l] = mine;
+  part[warp][lane] = mine;
   __syncthreads();
-  Cols acc = part[0][l];
-  for (int h = 1; h < kHalves; ++h) add_cols(acc, part[h][l]);
+  Cols acc = part[0][lane];
+  for (int w = 1; w < kSumWarps; ++w) add_cols(acc, part[w][lane]);
   return acc;
 }
 
 // CTAs [0, action_ctas): the action sums, one action each, from `parts` CTAs' tables.  The others: a
-// half-warp per window whose last run goes on: the run's sum is last[w] + first[w + 1] + ... up to
-// the window where it ends.  Runs over more than kLong windows are added by the whole CTA.
+// warp per window whose last run goes on: the run's sum is last[w] + first[w + 1] + ... up to the
+// window where it ends.  Runs over 32 windows or more are added by the whole CTA.
 __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32_t* __restrict__ first_key,
                                                                     const uint32_t* __restrict__ open_key,
                                                                     int64_t windows, int d,
@@ -443,82 +423,78 @@ __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32
                                                                     float* __restrict__ d_item, int action_ctas,
                                                                     const float* __restrict__ action_part, int parts,
                                                                     float* __restrict__ d_action) {
-  __shared__ Cols part[kHalves][16];
-  __shared__ int64_t long_end[kHalves];
-  const int half = threadIdx.x / 16, l = threadIdx.x % 16;
+  __shared__ Cols part[kSumWarps][32];
+  __shared__ int64_t long_end[kSumWarps];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if ((int)blockIdx.x < action_ctas) {
     const int a = (int)blockIdx.x;
-    for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
-      const int c = c0 + l * kCols;
-      const Cols acc = sum_halves(sum_range(action_part + (int64_t)a * d + c, (int64_t)parts * half / kHalves,
-                                            (int64_t)parts * (half + 1) / kHalves, (int64_t)action_ctas * d, c < d), part);
-      if (half == 0 && c < d) store_cols(d_action + (int64_t)a * d + c, acc);
+    for (int c0 = 0; c0 < d; c0 += 128) {
+      const int c = c0 + lane * 4;
+      const Cols acc = sum_warps(sum_range(action_part + (int64_t)a * d + c, (int64_t)parts * warp / kSumWarps,
+                                           (int64_t)parts * (warp + 1) / kSumWarps, (int64_t)action_ctas * d, c < d), part);
+      if (warp == 0 && c < d) store_cols(d_action + (int64_t)a * d + c, acc);
     }
     return;
   }
-  const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-  const int64_t w0 = (int64_t)(blockIdx.x - action_ctas) * kHalves, w = w0 + half;
+  const int64_t w0 = (int64_t)(blockIdx.x - action_ctas) * kSumWarps, w = w0 + warp;
   const uint32_t run = w + 1 < windows ? open_key[w] : kNone;
   int64_t end = 0;                                   // one behind the last window of the run (0: none to add)
+  bool is_long = false;
   if (run != kNone) {
     // window v > w holds a part of the run iff its first key is the run's
-    end = w + 1;
-    for (int i = 0; i < kLong; i += 16) {
-      const int64_t v = end + l;
-      const int more = __popc(__ballot_sync(mask, v < windows && first_key[v] == run) & mask);
-      end += more;
-      if (more < 16) break;
-    }
-    if (end == w + 1 + kLong) {                      // find the end, 16 probes at a time
-      int64_t lo = end, hi = windows;                // all windows before lo start with the run, hi does not
+    const int64_t v = w + 1 + lane;
+    const int more = __popc(__ballot_sync(0xffffffffu, v < windows && first_key[v] == run));
+    end = w + 1 + more;
+    is_long = more == 32;
+    if (is_long) {                                   // find the end, 32 probes at a time
+      int64_t lo = end, hi = windows;                // the windows before lo start with the run, hi does not
       while (lo < hi) {
-        const int64_t step = (hi - lo + 15) / 16, v = lo + l * step;
-        const int more = __popc(__ballot_sync(mask, v < hi && first_key[v] == run) & mask);
-        if (more == 0) break;
-        hi = min(hi, lo + more * step);
-        lo = lo + (more - 1) * step + 1;
+        const int64_t step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const int yes = __popc(__ballot_sync(0xffffffffu, at < hi && first_key[at] == run));
+        if (yes == 0) break;
+        hi = min(hi, lo + yes * step);
+        lo = lo + (yes - 1) * step + 1;
       }
       end = lo;
     }
   }
-  const bool is_long = end - w - 1 >= kLong;
-  if (l == 0) long_end[half] = is_long ? end : 0;
+  if (lane == 0) long_end[warp] = is_long ? end : 0;
   if (end > 0 && !is_long)
-    for (int c = l * kCols; c < d; c += 16 * kCols) {
+    for (int c = lane * 4; c < d; c += 128) {
       Cols acc = load_cols(last + w * d + c);
       add_cols(acc, sum_range(first + c, w + 1, end, d, true));
       store_cols(d_item + (int64_t)run * d + c, acc);
     }
   __syncthreads();
-  for (int i = 0; i < kHalves; ++i) {
+  for (int i = 0; i < kSumWarps; ++i) {
     const int64_t e = long_end[i], b = w0 + i;
     if (e == 0) continue;
     const int64_t cnt = e - b - 1;
     const uint32_t key = open_key[b];
-    for (int c0 = 0; c0 < d; c0 += 16 * kCols) {
-      const int c = c0 + l * kCols;
-      Cols acc = sum_range(first + c, b + 1 + cnt * half / kHalves, b + 1 + cnt * (half + 1) / kHalves, d, c < d);
-      if (half == 0 && c < d) add_cols(acc, load_cols(last + b * d + c));
-      acc = sum_halves(acc, part);
-      if (half == 0 && c < d) store_cols(d_item + (int64_t)key * d + c, acc);
+    for (int c0 = 0; c0 < d; c0 += 128) {
+      const int c = c0 + lane * 4;
+      Cols acc = sum_range(first + c, b + 1 + cnt * warp / kSumWarps, b + 1 + cnt * (warp + 1) / kSumWarps, d, c < d);
+      if (warp == 0 && c < d) add_cols(acc, load_cols(last + b * d + c));
+      acc = sum_warps(acc, part);
+      if (warp == 0 && c < d) store_cols(d_item + (int64_t)key * d + c, acc);
     }
   }
 }
 
 // part[CTA][action][d]: the sums of the CTA's contiguous events by action (more actions than the
 // window kernel's tables, or the action gradient alone).  Each warp adds its own contiguous part
-// into its own table in shared memory, two rows at a time, one after the other; the tables are added
-// in order.
+// into its own table in shared memory; the tables are added in order.
 template <class T>
 __global__ void action_rows_kernel(const T* __restrict__ dX, const int32_t* __restrict__ ids,
                                    const uint8_t* __restrict__ acts, int64_t n, int64_t per, int64_t vocab,
                                    int n_actions, int d, float* __restrict__ part, int* err) {
   extern __shared__ float4 tables[];                 // [warps][n_actions][32]
-  const int warp = threadIdx.x / 32, warps = blockDim.x / 32, lane = threadIdx.x % 32, l = lane % 16, h = lane / 16;
-  const int c = blockIdx.y * 16 * kCols + l * kCols;
+  constexpr int kBatch = batch_rows<T>();
+  const int warp = threadIdx.x / 32, warps = blockDim.x / 32, lane = threadIdx.x % 32;
+  const int c = blockIdx.y * 128 + lane * 4;
   const bool in = c < d;
-  const Table table{tables + warp * n_actions * 32};
-  table.clear(n_actions);
+  float4* mine = tables + warp * n_actions * 32 + lane;
+  for (int a = 0; a < n_actions; ++a) mine[a * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int64_t begin = min((int64_t)blockIdx.x * per, n), end = min(begin + per, n);
   const int64_t size = (end - begin + warps - 1) / warps;
   const int64_t wb = min(begin + warp * size, end), we = min(wb + size, end);
@@ -531,25 +507,23 @@ __global__ void action_rows_kernel(const T* __restrict__ dX, const int32_t* __re
       a = ok ? (int)acts[i0 + lane] : -1;
       bad |= !ok;
     }
-    for (int j = 0; j < cnt; j += 2 * kBatch) {      // rows j + 2 q + h
+#pragma unroll
+    for (int j = 0; j < 32; j += kBatch) {
+      if (j >= cnt) break;
       decltype(load_raw(dX)) x[kBatch];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q)
-        if (j + 2 * q + h < cnt && in) x[q] = load_raw(dX + (i0 + j + 2 * q + h) * d + c);
+        if (j + q < cnt && in) x[q] = load_raw(dX + (i0 + j + q) * d + c);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int aq = __shfl_sync(0xffffffffu, a, j + 2 * q + h);
-        const bool add = j + 2 * q + h < cnt && aq >= 0 && in;
-        if (add && h == 0) table.add(aq, l, widen(x[q]));
-        __syncwarp();
-        if (add && h == 1) table.add(aq, l, widen(x[q]));
-        __syncwarp();
+        const int aq = __shfl_sync(0xffffffffu, a, j + q);
+        if (j + q < cnt && aq >= 0 && in) add_to_table(mine + aq * 32, widen(x[q]));
       }
     }
   }
   if (bad && blockIdx.y == 0) atomicOr(err, DEV_ERR_INDEX);
   __syncthreads();
-  store_tables(tables, warps, n_actions, blockIdx.y * 16 * kCols, d, part + (int64_t)blockIdx.x * n_actions * d);
+  store_tables(tables, warps, n_actions, blockIdx.y * 128, d, part + (int64_t)blockIdx.x * n_actions * d);
 }
 
 int key_bits(int64_t vocab) {
@@ -565,11 +539,10 @@ int action_warps(int n_actions) { return std::max(1, std::min(kSumWarps, 256 / n
 int action_ctas(int64_t n) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(4 * device_info().sm_count, (n + 255) / 256));
 }
-// Windows: one per half-warp of the CTAs that are resident at once (three per SM, their registers'
-// limit: 16 tables take 64 KB of a CTA's shared memory), so that all have the same work.
+// Windows: one per warp of the CTAs that are resident at once, so that all have the same work.
 int64_t window_size(int64_t n) {
-  const int64_t halves = (int64_t)3 * device_info().sm_count * kHalves;
-  return std::max<int64_t>(kMinWin, (n + halves - 1) / halves);
+  const int64_t warps = (int64_t)kWindowCtas * device_info().sm_count * kSumWarps;
+  return std::max<int64_t>(kMinWin, (n + warps - 1) / warps);
 }
 
 template <class T>
@@ -580,7 +553,7 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
   int* err = device_status_word();
   const bool fused = d_item && d_action && n_actions <= kFusedActions;
   const int64_t win = window_size(n), windows = (n + win - 1) / win;
-  const int window_ctas = (int)((windows + kHalves - 1) / kHalves);
+  const int window_ctas = (int)((windows + kSumWarps - 1) / kSumWarps);
   const int parts = fused ? window_ctas : action_ctas(n);
   if (d_action && !fused) {
     const int warps = action_warps(n_actions);
@@ -646,7 +619,7 @@ size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, in
   v.last = c.take<float>(windows * d);
   v.first_key = c.take<uint32_t>(windows);
   v.open_key = c.take<uint32_t>(windows);
-  v.action_part = c.take<float>(std::max((size_t)action_ctas(n), (windows + kHalves - 1) / kHalves) * n_actions * d);
+  v.action_part = c.take<float>(std::max((size_t)action_ctas(n), (windows + kSumWarps - 1) / kSumWarps) * n_actions * d);
   if (w) *w = v;
   return c.bytes();
 }

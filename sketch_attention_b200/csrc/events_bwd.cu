@@ -17,20 +17,25 @@
 //
 // Bound by memory: dX read once, the item gradient written once.  The sort is one
 // cooperative launch (its CTAs exchange digit counts through memory between the passes'
-// steps): half of each CTA's warps sort, which waits on latency and leaves the memory
-// idle, and the other half zero the whole item gradient meanwhile (most of it stays
-// zero: a million items, 680K events); the rows with events are written over that.
+// steps) that waits on latency and leaves the memory idle, so a thread of each CTA zeroes
+// the whole item gradient meanwhile (most of it stays zero: a million items, 680K events)
+// with bulk stores out of shared memory, a bounded number in flight: written by ordinary
+// stores of half the warps, the zeros held up the sort's loads until they were all out
+// (40 us for a load, 124 us for both; zeros alone 78, sort alone 50).  The rows with events
+// are written over that.
 #include <algorithm>
 #include <mutex>
 
 #include "sa_internal.cuh"
+#include "tc_ptx.cuh"
 #include "tma_map.cuh"
 
 namespace sa {
 
 namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // of a CTA; as many again write zeros
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // sorting; one more warp zeroes
+constexpr int kZeroBytes = 16384, kZeroPending = 4;                 // a bulk store of zeros, and how many at once
 constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
@@ -93,13 +98,15 @@ struct SortArgs {
   int64_t n, per;            // events, and events per sorting CTA
   int bits, passes, ctas;    // of the keys; sorting CTAs
   uint32_t *keys[2], *events[2];   // the list after pass q is in buffer q & 1
-  int* hist;                 // [ctas][bins] digit counts of a pass, one array per pass parity
+  int* hist;                 // [ctas][bins] digit counts of a pass
+  int* before;               // [bins][ctas] the same of the earlier CTAs, and [bins] the digits' totals
   unsigned* counter;
-  float4* zero;              // the item gradient, and its 16-byte pieces
+  char* zero;                // the item gradient, and its bytes
   int64_t zeros;
   int* err;
 };
-constexpr int sort_smem(int bits) { return (kSortWarps + 3) * (1 << bits) * 4; }
+// zeros, then counts [warps][bins], digit totals [bins], and the earlier CTAs' counts [bins]
+constexpr int sort_smem(int bits) { return kZeroBytes + (kSortWarps + 2) * (1 << bits) * 4; }
 
 // One pass over the digit at `shift`: moves the CTA's events behind those with smaller digits, and
 // those with the same digit in earlier CTAs.  Each warp owns a contiguous part, counts its digits,
@@ -108,7 +115,7 @@ template <class In>
 __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int bits, int* smem, unsigned& round) {
   __shared__ int warp_sum[kSortWarps];
   const int bins = 1 << bits, cta = blockIdx.x;
-  int *wcnt = smem, *base = smem + kSortWarps * bins, *half = base + bins;   // [warps][bins], [bins], [2][bins]
+  int *wcnt = smem, *totals = smem + kSortWarps * bins, *base = totals + bins;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   for (int b = threadIdx.x; b < kSortWarps * bins; b += kSortThreads) wcnt[b] = 0;
   sort_sync();
@@ -146,40 +153,51 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
     }
   if (bad) atomicOr(s.err, DEV_ERR_INDEX);
   sort_sync();
-  // half[h][b]: events with digit b of the CTAs g = h mod 2; base[b]: of the earlier CTAs
-  int* hist = s.hist + (int64_t)(q & 1) * s.ctas * (1 << kMaxBits);
+  // the CTA's counts; then totals[b]: all events with digit b, base[b]: those of earlier CTAs
   for (int b = threadIdx.x; b < bins; b += kSortThreads) {
     int total = 0;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) total += wcnt[w * bins + b];
     if (s.ctas > 1) {
-      hist[(int64_t)cta * bins + b] = total;
+      s.hist[(int64_t)cta * bins + b] = total;
     } else {
+      totals[b] = total;
       base[b] = 0;
-      half[b] = total;
-      half[bins + b] = 0;
     }
   }
   if (s.ctas > 1) {
     grid_sync(s.counter, s.ctas, ++round, s.err);
-    // two halves of the CTAs, four bins per thread (bins >= 4)
-    const int quads = bins / 4, x = threadIdx.x % quads, h = threadIdx.x / quads;
-    int4 total = make_int4(0, 0, 0, 0), before = make_int4(0, 0, 0, 0);
-    if (h < 2) {
-#pragma unroll 16
-      for (int g = h; g < s.ctas; g += 2) {
-        const int4 c = __ldcg((const int4*)(hist + (int64_t)g * bins + 4 * x));
-        total.x += c.x; total.y += c.y; total.z += c.z; total.w += c.w;
-        if (g < cta) { before.x += c.x; before.y += c.y; before.z += c.z; before.w += c.w; }
+    // a warp per digit scans it over the CTAs (every CTA reading all counts takes twice as long)
+    for (int b = cta + s.ctas * warp; b < bins; b += s.ctas * kSortWarps) {
+      int carry = 0;
+      for (int g0 = 0; g0 < s.ctas; g0 += 128) {
+        int c[4], incl[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int g = g0 + 32 * x + lane;
+          c[x] = g < s.ctas ? __ldcg(s.hist + (int64_t)g * bins + b) : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          incl[x] = c[x];
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl[x], o);
+            if (lane >= o) incl[x] += y;
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int g = g0 + 32 * x + lane;
+          if (g < s.ctas) s.before[(int64_t)b * s.ctas + g] = carry + incl[x] - c[x];
+          carry += __shfl_sync(0xffffffffu, incl[x], 31);
+        }
       }
-      *(int4*)(half + h * bins + 4 * x) = total;
-      if (h == 0) *(int4*)(base + 4 * x) = before;
+      if (lane == 0) s.before[(int64_t)bins * s.ctas + b] = carry;
     }
-    sort_sync();
-    if (h == 1) {
-      int4 o = *(int4*)(base + 4 * x);
-      o.x += before.x; o.y += before.y; o.z += before.z; o.w += before.w;
-      *(int4*)(base + 4 * x) = o;
+    grid_sync(s.counter, s.ctas, ++round, s.err);
+    for (int b = threadIdx.x; b < bins; b += kSortThreads) {
+      base[b] = __ldcg(s.before + (int64_t)b * s.ctas + cta);
+      totals[b] = __ldcg(s.before + (int64_t)bins * s.ctas + b);
     }
   }
   sort_sync();
@@ -187,7 +205,7 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
   int carry = 0;
   for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
     const int b = b0 + threadIdx.x;
-    const int total = b < bins ? half[b] + half[bins + b] : 0;
+    const int total = b < bins ? totals[b] : 0;
     int incl = total;
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -219,8 +237,12 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
     for (int x = 0; x < kHeld; ++x) {
       if (i0 + 32 * x >= we) break;
       const bool there = i0 + 32 * x + lane < we;
-      const int digit = there ? (int)((key[x] >> shift) & (bins - 1)) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
+      const int digit = (int)((key[x] >> shift) & (bins - 1));
+      unsigned same = __ballot_sync(0xffffffffu, there);          // the lanes with this digit
+      for (int i = 0; i < bits; ++i) {
+        const unsigned set = __ballot_sync(0xffffffffu, (digit >> i) & 1);
+        same &= (digit >> i) & 1 ? set : ~set;
+      }
       const int rank = __popc(same & ((1u << lane) - 1));
       const int at = there ? mine[digit] : 0;
       __syncwarp();
@@ -238,17 +260,23 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
   else sort_sync();
 }
 
-__global__ void __launch_bounds__(2 * kSortThreads, 1) sort_events_kernel(SortArgs s) {
-  extern __shared__ __align__(16) int smem[];
+__global__ void __launch_bounds__(kSortThreads + 32, 1) sort_events_kernel(SortArgs s) {
+  extern __shared__ __align__(128) char smem_raw[];
   if (threadIdx.x >= kSortThreads) {
-    const int64_t stride = (int64_t)gridDim.x * kSortThreads;
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x - kSortThreads; i < s.zeros; i += stride)
-      __stcs(s.zero + i, zero);
+    const int lane = threadIdx.x % 32;
+    for (int i = lane; i < kZeroBytes / 16; i += 32) ((float4*)smem_raw)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      const int64_t step = (int64_t)gridDim.x * kZeroBytes;
+      for (int64_t at = (int64_t)blockIdx.x * kZeroBytes; at < s.zeros; at += step)
+        tc::bulk_store_limited<kZeroPending>(s.zero + at, smem_raw, (uint32_t)min((int64_t)kZeroBytes, s.zeros - at));
+      tc::bulk_store_wait();
+    }
     return;
   }
   if ((int)blockIdx.x >= s.ctas) return;
+  int* smem = (int*)(smem_raw + kZeroBytes);
   unsigned round = 0;
   for (int q = 0; q < s.passes; ++q) {
     const int shift = s.bits * q / s.passes, bits = s.bits * (q + 1) / s.passes - shift;
@@ -566,19 +594,19 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
   if (d_item) {
     const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
     SortArgs s{{ids, acts, vocab, n_actions}, n, 0, bits, passes, sort_ctas(n), {w.keys[0], w.keys[1]},
-               {w.events[0], w.events[1]}, w.hist, w.counter, (float4*)d_item, vocab * d / 4, err};
+               {w.events[0], w.events[1]}, w.hist, w.before, w.counter, (char*)d_item, vocab * d * 4, err};
     s.per = (n + s.ctas - 1) / s.ctas;
     set_smem_limit_once((const void*)sort_events_kernel, sort_smem(kMaxBits), &done[1], mu);
     const int smem = sort_smem((bits + passes - 1) / passes);
     if (s.ctas == 1) {
       SA_TIMED("sort_events_kernel", st,
-               (sort_events_kernel<<<device_info().sm_count, 2 * kSortThreads, smem, st>>>(s)));
+               (sort_events_kernel<<<device_info().sm_count, kSortThreads + 32, smem, st>>>(s)));
     } else {
       SA_CUDA(cudaMemsetAsync(w.counter, 0, sizeof(unsigned), st));
       void* args[] = {&s};
       SA_TIMED("sort_events_kernel", st,
                cudaLaunchCooperativeKernel((const void*)sort_events_kernel, dim3(device_info().sm_count),
-                                           dim3(2 * kSortThreads), args, (size_t)smem, st));
+                                           dim3(kSortThreads + 32), args, (size_t)smem, st));
     }
     const uint32_t *keys = w.keys[(passes - 1) & 1], *events = w.events[(passes - 1) & 1];
     if (fused) {
@@ -613,7 +641,8 @@ size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, in
     v.keys[i] = c.take<uint32_t>(rows);
     v.events[i] = c.take<uint32_t>(rows);
   }
-  v.hist = c.take<int>((size_t)2 * sort_ctas(n) << kMaxBits);
+  v.hist = c.take<int>((size_t)sort_ctas(n) << kMaxBits);
+  v.before = c.take<int>((size_t)(sort_ctas(n) + 1) << kMaxBits);
   v.counter = c.take<unsigned>(1);
   v.first = c.take<float>(windows * d);
   v.last = c.take<float>(windows * d);

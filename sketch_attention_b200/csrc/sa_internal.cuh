@@ -150,7 +150,8 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
 // Gradients of the event tables (events_bwd.cu).
 struct EventsBwdWork {
   uint32_t *keys[2], *events[2];   // [n] sorted item ids and their events, in two buffers
-  int* hist;             // [2, sort CTAs, 1024] digit counts
+  int* hist;             // [sort CTAs, 1024] digit counts
+  int* before;           // [1024, sort CTAs] counts of the earlier CTAs, and [1024] totals
   unsigned* counter;     // arrivals at the sort's barriers
   float *first, *last;   // [windows, d] sums of the runs that cross a window's begin and end
   uint32_t *first_key, *open_key;   // [windows] its first item, and the item whose run goes on behind it

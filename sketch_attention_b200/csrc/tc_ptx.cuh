@@ -93,6 +93,19 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* gsrc, uint
       ::"r"(smem_u32(smem_dst)), "l"((uint64_t)gsrc), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
+// Plain bulk store of this CTA's shared memory to global, in the issuing thread's bulk groups; waits
+// until at most kPending - 1 of its earlier stores are unfinished (the hardware's own completion).
+template <int kPending>
+__device__ __forceinline__ void bulk_store_limited(void* gdst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+               ::"l"((uint64_t)gdst), "r"(smem_u32(smem_src)), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(kPending - 1) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ TMA
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
                                             int32_t c0, int32_t c1) {

@@ -35,7 +35,7 @@ namespace sa {
 namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // sorting; one more warp zeroes
-constexpr int kZeroBytes = 16384, kZeroPending = 4;                 // a bulk store of zeros, and how many at once
+constexpr int kZeroBytes = 2048, kZeroPending = 4;                  // a bulk store of zeros, and how many at once
 constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
@@ -57,16 +57,13 @@ struct FromEvents {
   const uint8_t* acts;
   int64_t vocab;
   int n_actions;
-  __device__ uint32_t key(int64_t i) const { return event_key(ids, acts, i, vocab, n_actions); }
-  __device__ uint32_t event(int64_t i) const { return (uint32_t)i; }
+  __device__ uint2 at(int64_t i) const { return make_uint2(event_key(ids, acts, i, vocab, n_actions), (uint32_t)i); }
   __device__ bool outside(uint32_t key) const { return key == (uint32_t)vocab; }
 };
 struct FromList {
-  const uint32_t* keys;
-  const uint32_t* events;
+  const uint2* list;
   // written by other CTAs of this launch: not through L1
-  __device__ uint32_t key(int64_t i) const { return __ldcg(keys + i); }
-  __device__ uint32_t event(int64_t i) const { return __ldcg(events + i); }
+  __device__ uint2 at(int64_t i) const { return __ldcg(list + i); }
   __device__ bool outside(uint32_t) const { return false; }
 };
 
@@ -97,7 +94,7 @@ struct SortArgs {
   FromEvents in;
   int64_t n, per;            // events, and events per sorting CTA
   int bits, passes, ctas;    // of the keys; sorting CTAs
-  uint32_t *keys[2], *events[2];   // the list after pass q is in buffer q & 1
+  uint2* list[2];            // (key, event) after pass q in list[q & 1]: one scattered store per event
   int* hist;                 // [ctas][bins] digit counts of a pass
   int* before;               // [bins][ctas] the same of the earlier CTAs, and [bins] the digits' totals
   unsigned* counter;
@@ -126,13 +123,12 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
   bool bad = false;
   // the first kHeld keys of each lane stay in registers until they are placed (under the writes of
   // the zeros a load takes microseconds); longer parts are read again, kHeld at a time
-  uint32_t key[kHeld], ev[kHeld];
+  uint2 held[kHeld];
   auto load = [&](int64_t i0) {
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
       const int64_t i = i0 + 32 * x + lane;
-      key[x] = i < we ? in.key(i) : 0u;
-      ev[x] = i < we ? in.event(i) : 0u;
+      held[x] = i < we ? in.at(i) : make_uint2(0u, 0u);
     }
   };
   for (int64_t i0 = wb + 32 * kHeld; i0 < we; i0 += 32 * kHeld) {
@@ -140,16 +136,16 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
 #pragma unroll
     for (int x = 0; x < kHeld; ++x)
       if (i0 + 32 * x + lane < we) {
-        bad |= in.outside(key[x]);
-        atomicAdd(&mine[(key[x] >> shift) & (bins - 1)], 1);
+        bad |= in.outside(held[x].x);
+        atomicAdd(&mine[(held[x].x >> shift) & (bins - 1)], 1);
       }
   }
   load(wb);
 #pragma unroll
   for (int x = 0; x < kHeld; ++x)
     if (wb + 32 * x + lane < we) {
-      bad |= in.outside(key[x]);
-      atomicAdd(&mine[(key[x] >> shift) & (bins - 1)], 1);
+      bad |= in.outside(held[x].x);
+      atomicAdd(&mine[(held[x].x >> shift) & (bins - 1)], 1);
     }
   if (bad) atomicOr(s.err, DEV_ERR_INDEX);
   sort_sync();
@@ -230,14 +226,14 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
     }
     sort_sync();
   }
-  uint32_t *keys = s.keys[q & 1], *events = s.events[q & 1];
+  uint2* list = s.list[q & 1];
   for (int64_t i0 = wb; i0 < we; i0 += 32 * kHeld) {
     if (i0 > wb) load(i0);
 #pragma unroll
     for (int x = 0; x < kHeld; ++x) {
       if (i0 + 32 * x >= we) break;
       const bool there = i0 + 32 * x + lane < we;
-      const int digit = (int)((key[x] >> shift) & (bins - 1));
+      const int digit = (int)((held[x].x >> shift) & (bins - 1));
       unsigned same = __ballot_sync(0xffffffffu, there);          // the lanes with this digit
       for (int i = 0; i < bits; ++i) {
         const unsigned set = __ballot_sync(0xffffffffu, (digit >> i) & 1);
@@ -248,10 +244,7 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
       __syncwarp();
       if (there) {
         if (rank == 0) mine[digit] = at + __popc(same);
-        if ((unsigned)(at + rank) < (uint64_t)s.n) {
-          keys[at + rank] = key[x];
-          events[at + rank] = ev[x];
-        }
+        if ((unsigned)(at + rank) < (uint64_t)s.n) list[at + rank] = held[x];
       }
       __syncwarp();
     }
@@ -281,7 +274,7 @@ __global__ void __launch_bounds__(kSortThreads + 32, 1) sort_events_kernel(SortA
   for (int q = 0; q < s.passes; ++q) {
     const int shift = s.bits * q / s.passes, bits = s.bits * (q + 1) / s.passes - shift;
     if (q == 0) sort_pass(s.in, s, q, shift, bits, smem, round);
-    else sort_pass(FromList{s.keys[(q - 1) & 1], s.events[(q - 1) & 1]}, s, q, shift, bits, smem, round);
+    else sort_pass(FromList{s.list[(q - 1) & 1]}, s, q, shift, bits, smem, round);
   }
 }
 
@@ -333,9 +326,8 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;      // no item
 // added to the warp's table of action sums; the CTA's tables go to action_part[CTA][n_actions][d].
 template <class T, bool kActions>
 __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
-    const T* __restrict__ dX, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ events,
-    const uint8_t* __restrict__ acts, int64_t n, int64_t win, int64_t vocab, int n_actions, int d,
-    float* __restrict__ first, float* __restrict__ last, uint32_t* __restrict__ first_key,
+    const T* __restrict__ dX, const uint2* __restrict__ list, const uint8_t* __restrict__ acts, int64_t n, int64_t win, int64_t vocab,
+    int n_actions, int d, float* __restrict__ first, float* __restrict__ last, uint32_t* __restrict__ first_key,
     uint32_t* __restrict__ open_key, float* __restrict__ d_item, float* __restrict__ action_part) {
   extern __shared__ float4 tables[];                 // [kSumWarps][n_actions][32]
   constexpr int kBatch = batch_rows<T>();
@@ -350,20 +342,20 @@ __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
     if (p0 < p1) {
       const T* col = dX + (in ? c : 0);              // idle lanes read (and drop) the first columns
       Cols acc = zero_cols();
-      uint32_t run = p0 > 0 ? keys[p0 - 1] : kNone;  // key of the run that acc belongs to
-      const uint32_t behind = p1 < n ? keys[p1] : kNone;
+      uint32_t run = p0 > 0 ? list[p0 - 1].x : kNone;  // key of the run that acc belongs to
+      const uint32_t behind = p1 < n ? list[p1].x : kNone;
       bool inside = false;                           // a head was seen: acc starts at it
       // (an event number is below n, unless the sort gave up at a barrier)
-      auto event_at = [&](int64_t i) { const uint32_t e = events[i]; return e < (uint64_t)n ? e : 0u; };
-      uint32_t key_n = p0 + lane < p1 ? keys[p0 + lane] : kNone, ev_n = p0 + lane < p1 ? event_at(p0 + lane) : 0u;
-      if (lane == 0 && c0 == 0) first_key[w] = key_n;
+      auto list_at = [&](int64_t i) {
+        const uint2 x = list[i];
+        return make_uint2(x.x, x.y < (uint64_t)n ? x.y : 0u);
+      };
+      uint2 next = p0 + lane < p1 ? list_at(p0 + lane) : make_uint2(kNone, 0u);
+      if (lane == 0 && c0 == 0) first_key[w] = next.x;
       for (int64_t b = p0; b < p1; b += 32) {
         const int cnt = (int)min((int64_t)32, p1 - b);
-        const uint32_t key = key_n, ev = ev_n;
-        if (b + 32 + lane < p1) {                    // the next 32 positions, a step ahead
-          key_n = keys[b + 32 + lane];
-          ev_n = event_at(b + 32 + lane);
-        }
+        const uint32_t key = next.x, ev = next.y;
+        if (b + 32 + lane < p1) next = list_at(b + 32 + lane);   // the next 32 positions, a step ahead
         int act = -1;
         if (kActions && lane < cnt && key < (uint32_t)vocab) act = acts[ev];
         uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
@@ -593,8 +585,8 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
   }
   if (d_item) {
     const int bits = key_bits(vocab), passes = (bits + kMaxBits - 1) / kMaxBits;
-    SortArgs s{{ids, acts, vocab, n_actions}, n, 0, bits, passes, sort_ctas(n), {w.keys[0], w.keys[1]},
-               {w.events[0], w.events[1]}, w.hist, w.before, w.counter, (char*)d_item, vocab * d * 4, err};
+    SortArgs s{{ids, acts, vocab, n_actions}, n, 0, bits, passes, sort_ctas(n), {w.list[0], w.list[1]},
+               w.hist, w.before, w.counter, (char*)d_item, vocab * d * 4, err};
     s.per = (n + s.ctas - 1) / s.ctas;
     set_smem_limit_once((const void*)sort_events_kernel, sort_smem(kMaxBits), &done[1], mu);
     const int smem = sort_smem((bits + passes - 1) / passes);
@@ -608,18 +600,18 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
                cudaLaunchCooperativeKernel((const void*)sort_events_kernel, dim3(device_info().sm_count),
                                            dim3(kSortThreads + 32), args, (size_t)smem, st));
     }
-    const uint32_t *keys = w.keys[(passes - 1) & 1], *events = w.events[(passes - 1) & 1];
+    const uint2* list = w.list[(passes - 1) & 1];
     if (fused) {
       const int smem = kSumWarps * n_actions * 512;
       set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done[2], mu);
       SA_TIMED("window_rows_kernel", st,
                (window_rows_kernel<T, true><<<window_ctas, kSumThreads, smem, st>>>(
-                   dX, keys, events, acts, n, win, vocab, n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item,
+                   dX, list, acts, n, win, vocab, n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item,
                    w.action_part)));
     } else {
       SA_TIMED("window_rows_kernel", st,
                (window_rows_kernel<T, false><<<window_ctas, kSumThreads, 0, st>>>(
-                   dX, keys, events, acts, n, win, vocab, 0, d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr)));
+                   dX, list, acts, n, win, vocab, 0, d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr)));
     }
   }
   const int ac = d_action ? n_actions : 0;
@@ -637,10 +629,7 @@ size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, in
   const size_t rows = (size_t)std::max<int64_t>(n, 1);
   const int64_t win = window_size(n);
   const size_t windows = (size_t)std::max<int64_t>((n + win - 1) / win, 1);
-  for (int i = 0; i < 2; ++i) {
-    v.keys[i] = c.take<uint32_t>(rows);
-    v.events[i] = c.take<uint32_t>(rows);
-  }
+  for (int i = 0; i < 2; ++i) v.list[i] = c.take<uint2>(rows);
   v.hist = c.take<int>((size_t)sort_ctas(n) << kMaxBits);
   v.before = c.take<int>((size_t)(sort_ctas(n) + 1) << kMaxBits);
   v.counter = c.take<unsigned>(1);

@@ -149,7 +149,7 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
 
 // Gradients of the event tables (events_bwd.cu).
 struct EventsBwdWork {
-  uint32_t *keys[2], *events[2];   // [n] sorted item ids and their events, in two buffers
+  uint2* list[2];        // [n] (item id, event) in sorted order, in two buffers
   int* hist;             // [sort CTAs, 1024] digit counts
   int* before;           // [1024, sort CTAs] counts of the earlier CTAs, and [1024] totals
   unsigned* counter;     // arrivals at the sort's barriers

@@ -132,17 +132,16 @@ sa_status sa_tokenwise_run(const SaFwdArgs& a, const TokenwiseWork& w, cudaStrea
 struct TokenwiseBwdWork {
   Chunking chE;          // token chunks of the per-slice kernels (row statistics, E)
   Chunking chX;          // token chunks of the dX kernel
-  float* T;              // [d, d]
-  float* Pf;             // [k, d] folded prototypes, base-2 units
-  __nv_bfloat16 *Uhi, *Ulo;   // [kp, d] the same as hi + lo
+  float* Q;              // [k, d] P W_Q
+  __nv_bfloat16 *Uhi, *Ulo;   // [kp, d] folded prototypes U, base-2 units, as hi + lo
   __nv_bfloat16 *Hhi, *Hlo;   // [B, kp, d] dH as hi + lo
   float *c, *c2;         // [B, kp] dH . H, and ln2 times it
   float* lse2;           // [B, kp] log2 of the rows' sums of 2^z
   float2* stat_user;     // [B, 2, kp] (max, sum) of users inside one chunk
   float2* stat_slot;     // [G, 2, 2, kp] of the pieces of users that span chunks
   float* Epart;          // [G, k, d]
-  float *E, *dQ, *Q;     // [k, d]
-  float* gsplit;         // [kMaxSplit, d, d]
+  float* part_v;         // [CTAs, d, d] parts of sum H^T dS
+  float* part_qk;        // [CTAs, 2, d, d] parts of dW_Q and dW_K
 };
 size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, TokenwiseBwdWork* w);
 sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st);

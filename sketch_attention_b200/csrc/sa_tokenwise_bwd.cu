@@ -29,7 +29,6 @@
 #include <algorithm>
 #include <mutex>
 
-#include "gemm.cuh"
 #include "sa_internal.cuh"
 #include "tc_ptx.cuh"
 #include "tma_map.cuh"
@@ -735,77 +734,215 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   }
 }
 
-// ============================================================== operands
-// Rows 0 .. kp of the first part: U (base-2 units) as hi + lo, zero rows behind k.  Then, per
-// user and prototype, dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c (a user without events and
-// padding prototypes: zeros).  A warp computes four rows at once from W_V^T in shared memory.
-constexpr int PREP_THREADS = 256, PREP_WARPS = PREP_THREADS / 32;
-constexpr int PREP_SMEM = (DD * (DD + 1) + PREP_WARPS * 4 * DD) * 4;
+// ============================================================== rows of 128 columns
+// The products with the d x d weights, in fp32 FMA, 16 rows per CTA step: a thread has one of 128
+// columns and half of the 128 terms, 16 sums in registers, so a weight is read once (from L2) for
+// 16 products; the halves are added by a shuffle.  (The framework's tiled fp32 GEMM takes 12 us for
+// such a product at any k up to 1024; the eleven that fold the prototypes and carry E back to the
+// weights took two thirds of a small call.)
+constexpr int RB = 16, R_THREADS = 256;
 
-__global__ void __launch_bounds__(PREP_THREADS) tw_prepare_kernel(
-    const int64_t* __restrict__ off, int B, int k, int kp, float inv, const float* __restrict__ Pf,
-    const float* __restrict__ W_V, const float* __restrict__ dS, const float* __restrict__ H,
-    __nv_bfloat16* __restrict__ Uhi, __nv_bfloat16* __restrict__ Ulo, __nv_bfloat16* __restrict__ Hhi,
-    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2) {
-  extern __shared__ float sm[];
-  float* wt = sm;                                       // wt[e * 129 + d] = W_V[d, e]
-  float* rows = sm + DD * (DD + 1);                     // [warp][4][DD] rows of dS
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int e = threadIdx.x; e < DD * DD; e += PREP_THREADS) wt[(e % DD) * (DD + 1) + e / DD] = W_V[e];
-  __syncthreads();
-  for (int64_t e = (int64_t)blockIdx.x * PREP_THREADS + threadIdx.x; e < (int64_t)kp * DD;
-       e += (int64_t)gridDim.x * PREP_THREADS) {
-    const float x = e < (int64_t)k * DD ? Pf[e] : 0.f;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-    Uhi[e] = hi;
-    Ulo[e] = __float2bfloat16_rn(x - __bfloat162float(hi));
+// out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e]; the same in both half-warps
+template <bool kT>
+__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* __restrict__ W, float* out) {
+  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 64;
+#pragma unroll
+  for (int r = 0; r < RB; ++r) out[r] = 0.f;
+#pragma unroll 4
+  for (int e = e0; e < e0 + 64; e += 4) {
+    float4 w;
+    if (kT) w = __ldg((const float4*)(W + col * DD + e));
+    else w = make_float4(__ldg(W + e * DD + col), __ldg(W + (e + 1) * DD + col), __ldg(W + (e + 2) * DD + col),
+                         __ldg(W + (e + 3) * DD + col));
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      const float4 x = *(const float4*)&rows[r][e];
+      out[r] = fmaf(x.x, w.x, fmaf(x.y, w.y, fmaf(x.z, w.z, fmaf(x.w, w.w, out[r]))));
+    }
   }
-  float* mine = rows + warp * 4 * DD;
-  const int64_t groups = (int64_t)B * (kp / 4);
-  for (int64_t gr = (int64_t)blockIdx.x * PREP_WARPS + warp; gr < groups; gr += (int64_t)gridDim.x * PREP_WARPS) {
-    const int u = (int)(gr / (kp / 4)), j0 = (int)(gr % (kp / 4)) * 4;
-    const bool some = off[u + 1] > off[u];
-    __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < RB; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
+}
+
+// rows[r] = src[r] (d floats each) for r < have, else zeros
+__device__ __forceinline__ void load_block(float (*rows)[DD], const float* __restrict__ src, int have) {
+  for (int i = threadIdx.x; i < RB * DD / 4; i += R_THREADS)
+    ((float4*)rows)[i] = i / (DD / 4) < have ? __ldg((const float4*)src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// acc[8][8] += sum_r a[r][8 ty ..] b[r][8 tx ..]: a thread's tile of a^T b
+__device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)[DD], float (*acc)[8]) {
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+#pragma unroll 2
+  for (int r = 0; r < RB; ++r) {
+    const float4 a0 = *(const float4*)&a[r][8 * ty], a1 = *(const float4*)&a[r][8 * ty + 4];
+    const float4 b0 = *(const float4*)&b[r][8 * tx], b1 = *(const float4*)&b[r][8 * tx + 4];
+    const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        mine[r * DD + 32 * x + lane] =
-            some && j0 + r < k ? dS[((int64_t)u * k + j0 + r) * DD + 32 * x + lane] : 0.f;
-    __syncwarp();
-    float acc[4][4] = {};
-    for (int e = 0; e < DD; e += 4) {
-      float4 s[4];
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[r] = *(const float4*)(mine + r * DD + e);
+      for (int x = 0; x < 8; ++x) acc[i][x] = fmaf(av[i], bv[x], acc[i][x]);
+  }
+}
+__device__ __forceinline__ void store_outer(float* __restrict__ part, const float (*acc)[8]) {
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+  for (int i = 0; i < 8; ++i) {
+    float4* dst = (float4*)(part + (8 * ty + i) * DD + 8 * tx);
+    dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+  }
+}
+
+// CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
+// The others, 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
+// (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
+__global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
+    const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
+    const float* __restrict__ W_Q, const float* __restrict__ W_K, const float* __restrict__ W_V,
+    const float* __restrict__ dS, const float* __restrict__ H, float* __restrict__ Q, __nv_bfloat16* __restrict__ Uhi,
+    __nv_bfloat16* __restrict__ Ulo, __nv_bfloat16* __restrict__ Hhi, __nv_bfloat16* __restrict__ Hlo,
+    float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v) {
+  __shared__ float a[RB][DD], b[RB][DD], dots[R_THREADS / 32][RB];
+  const int warp = threadIdx.x / 32, col = warp * 16 + threadIdx.x % 16, h = threadIdx.x % 32 / 16;
+  const int groups = kp / RB;
+  float v[RB];
+  if ((int)blockIdx.x < groups) {
+    const int j0 = blockIdx.x * RB;
+    load_block(a, P + (int64_t)j0 * DD, k - j0);
+    __syncthreads();
+    rows_product<false>(a, W_Q, v);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float w = wt[(e + y) * (DD + 1) + 32 * x + lane];
+    for (int r = 0; r < RB; ++r) {
+      if (r / 8 != h) continue;              // each half-warp keeps 8 of the rows
+      b[r][col] = v[r];
+      if (j0 + r < k) Q[(int64_t)(j0 + r) * DD + col] = v[r];
+    }
+    __syncthreads();
+    rows_product<true>(b, W_K, v);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r][x] = fmaf((&s[r].x)[y], w, acc[r][x]);
+    for (int r = 0; r < RB; ++r) {
+      if (r / 8 != h) continue;
+      const float x = v[r] * u_scale;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+      Uhi[(int64_t)(j0 + r) * DD + col] = hi;
+      Ulo[(int64_t)(j0 + r) * DD + col] = __float2bfloat16_rn(x - __bfloat162float(hi));
+    }
+    return;
+  }
+  const int part = blockIdx.x - groups, parts = gridDim.x - groups;
+  float dwv[8][8] = {};
+  for (int64_t g = part; g < (int64_t)B * groups; g += parts) {
+    const int u = (int)(g / groups), j0 = (int)(g % groups) * RB;
+    const int have = off[u + 1] > off[u] ? k - j0 : 0;
+    const int64_t in = ((int64_t)u * k + j0) * DD, out = ((int64_t)u * kp + j0) * DD;
+    __syncthreads();
+    load_block(a, dS + in, have);
+    load_block(b, H + in, have);
+    __syncthreads();
+    rows_product<true>(a, W_V, v);
+#pragma unroll
+    for (int r = 0; r < RB; ++r) {
+      v[r] *= inv;
+      float dot = v[r] * b[r][col];
+      for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (threadIdx.x % 32 == 0) dots[warp][r] = dot;
+      if (r / 8 != h) continue;
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v[r]);
+      Hhi[out + r * DD + col] = hi;
+      Hlo[out + r * DD + col] = __float2bfloat16_rn(v[r] - __bfloat162float(hi));
+    }
+    add_outer(b, a, dwv);
+    __syncthreads();
+    if (threadIdx.x < RB) {
+      float c = 0.f;
+      for (int w = 0; w < R_THREADS / 32; ++w) c += dots[w][threadIdx.x];
+      const int64_t row = (int64_t)u * kp + j0 + threadIdx.x;
+      cj[row] = c;
+      c2[row] = kLn2 * c;
+    }
+  }
+  store_outer(part_v + (int64_t)part * DD * DD, dwv);
+}
+
+// 16 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
+// the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
+__global__ void __launch_bounds__(R_THREADS) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
+                                                               const float* __restrict__ P, const float* __restrict__ Q,
+                                                               const float* __restrict__ W_Q,
+                                                               const float* __restrict__ W_K, float* __restrict__ dP,
+                                                               float* __restrict__ part_qk) {
+  __shared__ float e[RB][DD], q[RB][DD], dq[RB][DD];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = warp * 16 + lane % 16, h = lane / 16;
+  float dwq[8][8] = {}, dwk[8][8] = {};
+  for (int j0 = blockIdx.x * RB; j0 < k; j0 += gridDim.x * RB) {
+    __syncthreads();
+    for (int r = warp; r < RB; r += R_THREADS / 32) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j0 + r < k) {
+        const float* src = Epart + (int64_t)(j0 + r) * DD + lane * 4;
+#pragma unroll 8
+        for (int g = 0; g < G; ++g) {
+          const float4 x = *(const float4*)(src + (int64_t)g * k * DD);
+          s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
         }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t in = ((int64_t)u * k + j0 + r) * DD, out = ((int64_t)u * kp + j0 + r) * DD;
-      float dot = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float v = acc[r][x] * inv;
-        if (some && j0 + r < k) dot = fmaf(v, H[in + 32 * x + lane], dot);
-        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-        Hhi[out + 32 * x + lane] = hi;
-        Hlo[out + 32 * x + lane] = __float2bfloat16_rn(v - __bfloat162float(hi));
       }
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) {
-        cj[(int64_t)u * kp + j0 + r] = dot;
-        c2[(int64_t)u * kp + j0 + r] = kLn2 * dot;
-      }
+      *(float4*)&e[r][lane * 4] = s;
     }
+    load_block(q, Q + (int64_t)j0 * DD, k - j0);
+    __syncthreads();
+    add_outer(e, q, dwk);
+    float v[RB];
+    rows_product<false>(e, W_K, v);
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      if (r / 8 == h) dq[r][col] = v[r] * rs;
+    __syncthreads();                         // and q is no longer read: the rows of P replace it
+    load_block(q, P + (int64_t)j0 * DD, k - j0);
+    rows_product<true>(dq, W_Q, v);
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+      if (r / 8 == h && j0 + r < k) dP[(int64_t)(j0 + r) * DD + col] = v[r];
+    __syncthreads();
+    add_outer(q, dq, dwq);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) dwk[i][x] *= rs;
+  store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq);
+  store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk);
+}
+
+// dW_V = i times the sum of its parts, dW_Q and dW_K the sums of theirs: a CTA per 128 values, its
+// 8 warps over the parts, added in order
+__global__ void __launch_bounds__(R_THREADS) tw_sum_kernel(const float* __restrict__ part_v, int n_v, float inv,
+                                                           const float* __restrict__ part_qk, int n_qk,
+                                                           float* __restrict__ dW_V, float* __restrict__ dW_Q,
+                                                           float* __restrict__ dW_K) {
+  __shared__ float4 sums[R_THREADS / 32][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int which = blockIdx.x / DD, at = blockIdx.x % DD * DD + lane * 4;
+  const float* src = (which == 0 ? part_v : part_qk + (which - 1) * DD * DD) + at;
+  const int n = which == 0 ? n_v : n_qk;
+  const int64_t pitch = which == 0 ? DD * DD : 2 * DD * DD;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = n * warp / 8; i < n * (warp + 1) / 8; ++i) {
+    const float4 x = *(const float4*)(src + i * pitch);
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0) return;
+  for (int w = 1; w < R_THREADS / 32; ++w) {
+    const float4 x = sums[w][lane];
+    s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+  }
+  const float f = which == 0 ? inv : 1.f;
+  float* dst = which == 0 ? dW_V : which == 1 ? dW_Q : dW_K;
+  *(float4*)(dst + at) = make_float4(f * s.x, f * s.y, f * s.z, f * s.w);
 }
 
 int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
@@ -814,6 +951,9 @@ int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
 Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
+// CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again)
+int value_parts(int B, int k) { return std::min(B * (padded_k(k) / RB), 128); }
+int weight_parts(int k) { return std::min((k + RB - 1) / RB, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
 
 sa_status map_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_rows) {
@@ -828,46 +968,34 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
   v.chE = slice_chunks(n, k);
   v.chX = token_chunks(n);
   const size_t G = (size_t)std::max(v.chE.G, 1);
-  v.T = c.take<float>(dd);
-  v.Pf = c.take<float>(kd);
+  v.Q = c.take<float>(kd);
   for (__nv_bfloat16** p : {&v.Uhi, &v.Ulo}) *p = c.take<__nv_bfloat16>(kp * d);
   for (__nv_bfloat16** p : {&v.Hhi, &v.Hlo}) *p = c.take<__nv_bfloat16>((size_t)B * kp * d);
   for (float** p : {&v.c, &v.c2, &v.lse2}) *p = c.take<float>((size_t)B * kp);
   v.stat_user = c.take<float2>((size_t)B * 2 * kp);
   v.stat_slot = c.take<float2>(G * 4 * kp);
   v.Epart = c.take<float>(G * kd);
-  for (float** p : {&v.E, &v.dQ, &v.Q}) *p = c.take<float>(kd);
-  v.gsplit = c.take<float>((size_t)kMaxSplit * dd);
+  v.part_v = c.take<float>(value_parts(B, k) * dd);
+  v.part_qk = c.take<float>(weight_parts(k) * 2 * dd);
   if (w) *w = v;
   return c.bytes();
 }
 
 sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st) {
-  static unsigned long long done_s = 0, done_e = 0, done_x = 0, done_p = 0;
+  static unsigned long long done_s = 0, done_e = 0, done_x = 0;
   static std::mutex mu;
   set_smem_limit_once((const void*)tw_lse_kernel, S_SMEM, &done_s, mu);
   set_smem_limit_once((const void*)tw_e_kernel, E_SMEM, &done_e, mu);
   set_smem_limit_once((const void*)tw_dx_kernel, X_SMEM, &done_x, mu);
-  set_smem_limit_once((const void*)tw_prepare_kernel, PREP_SMEM, &done_p, mu);
-  const int kp = padded_k(a.k), slices = kp / TILE;
+  const int kp = padded_k(a.k), slices = kp / TILE, n_v = value_parts(a.B, a.k), n_qk = weight_parts(a.k);
   const float inv = 1.f / (1.f + a.eps);                // m = 1 for a user with events
+  const float rs = 1.f / sqrtf((float)a.d);
   sa_status s;
-  // dW_V = i sum_u H^T dS
-  Gemm gv;
-  gv.M = a.d; gv.N = a.d; gv.K = a.B * a.k;
-  gv.A = a.H; gv.lda = a.d; gv.transA = true;
-  gv.B = a.dS; gv.ldb = a.d;
-  gv.C = a.dW_V; gv.ldc = a.d; gv.alpha = inv; gv.tag = "gemm:dW_V";
-  gv.split_k = gemm_split_for(a.d, a.d, gv.K, kMaxSplit);
-  gv.split_ws = w.gsplit;
-  if ((s = gemm(gv, st)) != SA_OK) return s;
+  SA_TIMED("tw_prepare_kernel", st,
+           (tw_prepare_kernel<<<kp / RB + n_v, R_THREADS, 0, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
+                                                                   a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi, w.Ulo,
+                                                                   w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
   if (a.n_total > 0) {
-    if ((s = sa_fold(a.k, a.d, a.P, a.W_Q, a.W_K, w.T, w.Pf, nullptr, st)) != SA_OK) return s;
-    const int64_t warps = std::max<int64_t>((int64_t)a.B * (kp / 4), 1);
-    const unsigned prep = (unsigned)std::min<int64_t>((warps + PREP_WARPS - 1) / PREP_WARPS, 2 * device_info().sm_count);
-    SA_TIMED("tw_prepare_kernel", st,
-             (tw_prepare_kernel<<<prep, PREP_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, w.Pf, a.W_V, a.dS,
-                                                                       a.H, w.Uhi, w.Ulo, w.Hhi, w.Hlo, w.c, w.c2)));
     CUtensorMap tmX, tmU, tmUlo, tmH, tmHlo, tmU64, tmUlo64, tmH64;
     const int64_t hrows = (int64_t)a.B * kp;
     if ((s = map_rows(&tmX, a.X, a.n_total, 128)) != SA_OK) return s;
@@ -890,14 +1018,12 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
     SA_TIMED("tw_e_kernel", st,
              (tw_e_kernel<<<w.chE.G * slices, E_THREADS, E_SMEM, st>>>(tmX, tmU, tmUlo, tmH, tmHlo, ep)));
   }
-  SaBwdWork gw{};
-  gw.chE = w.chE;
-  gw.Epart = w.Epart;
-  gw.E = w.E;
-  gw.dQ = w.dQ;
-  gw.Q = w.Q;
-  gw.gsplit = w.gsplit;
-  return sa_bwd_weight_grads(a, gw, st);
+  SA_TIMED("tw_weights_kernel", st,
+           (tw_weights_kernel<<<n_qk, R_THREADS, 0, st>>>(a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q, a.W_K, a.dP,
+                                                          w.part_qk)));
+  SA_TIMED("tw_sum_kernel", st,
+           (tw_sum_kernel<<<3 * DD, R_THREADS, 0, st>>>(w.part_v, n_v, inv, w.part_qk, n_qk, a.dW_V, a.dW_Q, a.dW_K)));
+  return SA_OK;
 }
 
 }  // namespace sa

@@ -237,25 +237,47 @@ def _need_cuda(*ts):
 
 def _need(name: str, t: torch.Tensor, dtype, shape, device):
     """t is a contiguous CUDA tensor of that dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() and t.is_cuda:
+        return t
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+_SAME_PLACE = contextlib.nullcontext()
+# torch.cuda.current_stream builds a Stream object, as long as two kernel launches take
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _at(device, stream):
     """Runs a call on its tensors' device and on `stream`: buffers allocated inside belong to that
     stream, so the allocator hands them out again only behind the call's kernels."""
     if stream is None:
-        return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _SAME_PLACE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
+
+
+def _raw_stream(device, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _current_raw_stream(device.index)
+
+
+def _workspace(given: Optional[torch.Tensor], size: int, device) -> torch.Tensor:
+    """The caller's workspace if it is large enough, else a new one (at least one byte)."""
+    if given is None:
+        return torch.empty(size or 1, dtype=torch.uint8, device=device)
+    if not given.is_cuda or not given.is_contiguous() or given.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return given if given.nbytes >= size else torch.empty(size, dtype=torch.uint8, device=device)
 
 
 # --------------------------------------------------------------------------
@@ -355,25 +377,25 @@ def sa_backward_tokenwise(X: torch.Tensor, offsets, P, W_Q, W_K, W_V, eps: float
     k, d = P.shape
     dev, f32 = X.device, torch.float32
     _need("X", X, torch.bfloat16, (n, d), dev)
-    for name, t, shape in (("P", P, (k, d)), ("W_Q", W_Q, (d, d)), ("W_K", W_K, (d, d)), ("W_V", W_V, (d, d)),
-                           ("H", H, (B, k, d)), ("dS", dS, (B, k, d))):
-        _need(name, t, f32, shape, dev)
+    _need("P", P, f32, (k, d), dev)
+    _need("W_Q", W_Q, f32, (d, d), dev)
+    _need("W_K", W_K, f32, (d, d), dev)
+    _need("W_V", W_V, f32, (d, d), dev)
+    _need("H", H, f32, (B, k, d), dev)
+    _need("dS", dS, f32, (B, k, d), dev)
     if offsets_dev is not None:
         _need("offsets_dev", offsets_dev, torch.int64, (B + 1,), dev)
     with _at(dev, stream):
         res = {}
-        for name, dt, shape in (("dX", torch.bfloat16, (n, d)), ("dP", f32, (k, d)), ("dW_Q", f32, (d, d)),
-                                ("dW_K", f32, (d, d)), ("dW_V", f32, (d, d))):
+        for name, like in (("dX", X), ("dP", P), ("dW_Q", W_Q), ("dW_K", W_K), ("dW_V", W_V)):
             t = out.get(name) if out else None
-            res[name] = torch.empty(shape, dtype=dt, device=dev) if t is None else _need(name, t, dt, shape, dev)
-        ws_bytes = lib.sa_backward_tokenwise_workspace(B, n, k, d, SA_BF16)
-        if workspace is None or workspace.numel() < ws_bytes:
-            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
+            res[name] = torch.empty_like(like) if t is None else _need(name, t, like.dtype, like.shape, dev)
+        ws = _workspace(workspace, lib.sa_backward_tokenwise_workspace(B, n, k, d, SA_BF16), dev)
         offd = _dev_i64(off, dev, offsets_dev)
-        st = lib.sa_backward_tokenwise(_p(X), SA_BF16, _hp(off), _p(offd), B, k, d, _p(P), _p(W_Q), _p(W_K), _p(W_V),
-                                       float(eps), _p(H), _p(dS), _p(res["dX"]), _p(res["dP"]), _p(res["dW_Q"]),
-                                       _p(res["dW_K"]), _p(res["dW_V"]), _p(workspace), workspace.numel(),
-                                       _stream(stream))
+        st = lib.sa_backward_tokenwise(X.data_ptr(), SA_BF16, off.ctypes.data, offd.data_ptr(), B, k, d, P.data_ptr(),
+                                       W_Q.data_ptr(), W_K.data_ptr(), W_V.data_ptr(), eps, H.data_ptr(), dS.data_ptr(),
+                                       *(t.data_ptr() for t in res.values()), ws.data_ptr(), ws.nbytes,
+                                       _raw_stream(dev, stream))
         _check("sa_backward_tokenwise", st)
     return res
 
@@ -586,12 +608,13 @@ def sa_gather_events_backward(item_ids: torch.Tensor, action_ids: torch.Tensor, 
                 res[name] = _need(name, t, torch.float32, (rows, d), dev)
             elif want:
                 res[name] = torch.empty(rows, d, device=dev)
-        ws_bytes = lib.sa_gather_events_backward_workspace(n, vocab, n_actions, d)
-        if workspace is None or workspace.numel() < ws_bytes:
-            workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=dev)
-        st = lib.sa_gather_events_backward(_p(item_ids), _p(action_ids), n, _p(dX), _dtype_code(dX), vocab, n_actions,
-                                           d, _p(res.get("d_item")), _p(res.get("d_action")), _p(workspace),
-                                           workspace.numel(), _stream(stream))
+        ws = _workspace(workspace, lib.sa_gather_events_backward_workspace(n, vocab, n_actions, d), dev)
+        item, action = res.get("d_item"), res.get("d_action")
+        st = lib.sa_gather_events_backward(item_ids.data_ptr(), action_ids.data_ptr(), n, dX.data_ptr(),
+                                           _dtype_code(dX), vocab, n_actions, d,
+                                           None if item is None else item.data_ptr(),
+                                           None if action is None else action.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                           _raw_stream(dev, stream))
         _check("sa_gather_events_backward", st)
     return res
 
@@ -640,9 +663,10 @@ def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
                         ("grad_scale", grad_scale, torch.float32)):
         if t is not None:
             _need(name, t.view(-1), dt, (1,), dev)
-    cfg = AdamWConfigC(lr, beta1, beta2, eps, step, _p(step_dev), _p(lr_dev), _p(grad_scale))
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    cfg = AdamWConfigC(lr, beta1, beta2, eps, step, at(step_dev), at(lr_dev), at(grad_scale))
     with _at(dev, stream):
-        _check("sa_adamw_step", lib.sa_adamw_step(tensors.c, len(tensors.tensors), ctypes.byref(cfg), _stream(stream)))
+        _check("sa_adamw_step", lib.sa_adamw_step(tensors.c, len(tensors.tensors), cfg, _raw_stream(dev, stream)))
 
 
 def sa_gather_events_fused_workspace(n_actions: int, d: int = 128, d_ff: int = 256) -> int:

@@ -735,21 +735,22 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 }
 
 // ============================================================== rows of 128 columns
-// The products with the d x d weights, in fp32 FMA, 16 rows per CTA step: a thread has one of 128
-// columns and half of the 128 terms, 16 sums in registers, so a weight is read once (from L2) for
-// 16 products; the halves are added by a shuffle.  (The framework's tiled fp32 GEMM takes 12 us for
+// The products with the d x d weights, in fp32 FMA, 8 rows per CTA step: a thread has one of 128
+// columns and half of the 128 terms, 8 sums in registers, so a weight is read once (from L2) for
+// 8 products; the halves are added by a shuffle.  (The framework's tiled fp32 GEMM takes 12 us for
 // such a product at any k up to 1024; the eleven that fold the prototypes and carry E back to the
 // weights took two thirds of a small call.)
-constexpr int RB = 16, R_THREADS = 256;
+constexpr int RB = 8, R_THREADS = 256;
 
 // out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e]; the same in both half-warps
 template <bool kT>
 __device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* __restrict__ W, float* out) {
-  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 64;
+  // the half-warps take every other four terms: their broadcast reads of a row are neighbours
+  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 4;
 #pragma unroll
   for (int r = 0; r < RB; ++r) out[r] = 0.f;
-#pragma unroll 4
-  for (int e = e0; e < e0 + 64; e += 4) {
+#pragma unroll 8
+  for (int e = e0; e < DD; e += 8) {
     float4 w;
     if (kT) w = __ldg((const float4*)(W + col * DD + e));
     else w = make_float4(__ldg(W + e * DD + col), __ldg(W + (e + 1) * DD + col), __ldg(W + (e + 2) * DD + col),
@@ -795,8 +796,8 @@ __device__ __forceinline__ void store_outer(float* __restrict__ part, const floa
   }
 }
 
-// CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others, 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
+// CTAs [0, kp / 8): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
+// The others, 8 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
 // (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
 __global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
     rows_product<false>(a, W_Q, v);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      if (r / 8 != h) continue;              // each half-warp keeps 8 of the rows
+      if (r / (RB / 2) != h) continue;       // each half-warp keeps half of the rows
       b[r][col] = v[r];
       if (j0 + r < k) Q[(int64_t)(j0 + r) * DD + col] = v[r];
     }
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
     rows_product<true>(b, W_K, v);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
-      if (r / 8 != h) continue;
+      if (r / (RB / 2) != h) continue;
       const float x = v[r] * u_scale;
       const __nv_bfloat16 hi = __float2bfloat16_rn(x);
       Uhi[(int64_t)(j0 + r) * DD + col] = hi;
@@ -848,7 +849,7 @@ __global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
       float dot = v[r] * b[r][col];
       for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if (threadIdx.x % 32 == 0) dots[warp][r] = dot;
-      if (r / 8 != h) continue;
+      if (r / (RB / 2) != h) continue;
       const __nv_bfloat16 hi = __float2bfloat16_rn(v[r]);
       Hhi[out + r * DD + col] = hi;
       Hlo[out + r * DD + col] = __float2bfloat16_rn(v[r] - __bfloat162float(hi));
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
   store_outer(part_v + (int64_t)part * DD * DD, dwv);
 }
 
-// 16 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
+// 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
 // the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
 __global__ void __launch_bounds__(R_THREADS) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
                                                                const float* __restrict__ P, const float* __restrict__ Q,
@@ -897,13 +898,13 @@ __global__ void __launch_bounds__(R_THREADS) tw_weights_kernel(int k, int G, flo
     rows_product<false>(e, W_K, v);
 #pragma unroll
     for (int r = 0; r < RB; ++r)
-      if (r / 8 == h) dq[r][col] = v[r] * rs;
+      if (r / (RB / 2) == h) dq[r][col] = v[r] * rs;
     __syncthreads();                         // and q is no longer read: the rows of P replace it
     load_block(q, P + (int64_t)j0 * DD, k - j0);
     rows_product<true>(dq, W_Q, v);
 #pragma unroll
     for (int r = 0; r < RB; ++r)
-      if (r / 8 == h && j0 + r < k) dP[(int64_t)(j0 + r) * DD + col] = v[r];
+      if (r / (RB / 2) == h && j0 + r < k) dP[(int64_t)(j0 + r) * DD + col] = v[r];
     __syncthreads();
     add_outer(q, dq, dwq);
   }

@@ -735,49 +735,79 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 }
 
 // ============================================================== rows of 128 columns
-// The products with the d x d weights, in fp32 FMA, 8 rows per CTA step: a thread has one of 128
-// columns and half of the 128 terms, 8 sums in registers, so a weight is read once (from L2) for
-// 8 products; the halves are added by a shuffle.  (The framework's tiled fp32 GEMM takes 12 us for
-// such a product at any k up to 1024; the eleven that fold the prototypes and carry E back to the
-// weights took two thirds of a small call.)
-constexpr int RB = 8, R_THREADS = 256;
+// The products with the d x d weights, in fp32 FMA, R rows per CTA step (the framework's tiled fp32
+// GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
+// carry E back to the weights took two thirds of a small call).  A weight matrix lies in shared
+// memory (read once per CTA), [term][column] with a pitch of 132; a thread has four columns of R / 8
+// rows, a warp all columns, so its reads of a row are broadcasts and a row's sums are a shuffle.
+constexpr int R_THREADS = 256, W_PITCH = DD + 4;
+constexpr uint32_t W_BYTES = DD * W_PITCH * 4;
+constexpr int RP = 32, RW = 16;              // rows per step of the prepare and the weights kernel
+constexpr uint32_t PREP_SMEM = 2 * W_BYTES + 2 * RP * DD * 4, WEIGHTS_SMEM = 2 * W_BYTES + 3 * RW * DD * 4;
 
-// out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e]; the same in both half-warps
-template <bool kT>
-__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* __restrict__ W, float* out) {
-  // the half-warps take every other four terms: their broadcast reads of a row are neighbours
-  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 4;
-#pragma unroll
-  for (int r = 0; r < RB; ++r) out[r] = 0.f;
+// w[e][c] = W[e][c]
+__device__ __forceinline__ void load_weight(float* w, const float* __restrict__ W) {
 #pragma unroll 8
-  for (int e = e0; e < DD; e += 8) {
-    float4 w;
-    if (kT) w = __ldg((const float4*)(W + col * DD + e));
-    else w = make_float4(__ldg(W + e * DD + col), __ldg(W + (e + 1) * DD + col), __ldg(W + (e + 2) * DD + col),
-                         __ldg(W + (e + 3) * DD + col));
-#pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      const float4 x = *(const float4*)&rows[r][e];
-      out[r] = fmaf(x.x, w.x, fmaf(x.y, w.y, fmaf(x.z, w.z, fmaf(x.w, w.w, out[r]))));
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RB; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
+  for (int i = threadIdx.x; i < DD * DD / 4; i += R_THREADS)
+    *(float4*)(w + i / 32 * W_PITCH + i % 32 * 4) = __ldg((const float4*)W + i);
 }
-
+// w[e][c] = W[c][e]: a warp stores one term of 32 columns at a time
+__device__ __forceinline__ void load_weight_transposed(float* w, const float* __restrict__ W) {
+#pragma unroll 8
+  for (int i = threadIdx.x; i < DD * DD / 4; i += R_THREADS) {
+    const int c = i % DD, e = i / DD * 4;
+    const float4 x = __ldg((const float4*)(W + c * DD + e));
+    w[e * W_PITCH + c] = x.x;
+    w[(e + 1) * W_PITCH + c] = x.y;
+    w[(e + 2) * W_PITCH + c] = x.z;
+    w[(e + 3) * W_PITCH + c] = x.w;
+  }
+}
 // rows[r] = src[r] (d floats each) for r < have, else zeros
+template <int R>
 __device__ __forceinline__ void load_block(float (*rows)[DD], const float* __restrict__ src, int have) {
-  for (int i = threadIdx.x; i < RB * DD / 4; i += R_THREADS)
+#pragma unroll
+  for (int i = threadIdx.x; i < R * DD / 4; i += R_THREADS)
     ((float4*)rows)[i] = i / (DD / 4) < have ? __ldg((const float4*)src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-// acc[8][8] += sum_r a[r][8 ty ..] b[r][8 tx ..]: a thread's tile of a^T b
+// out[x][.] = sum_e rows[R / 8 warp + x][e] w[e][4 lane ..]
+template <int R>
+__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float (*out)[4]) {
+  constexpr int N = R / 8;
+  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N;
+#pragma unroll
+  for (int x = 0; x < N; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[x][i] = 0.f;
+#pragma unroll 4
+  for (int e = 0; e < DD; e += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) v[y] = *(const float4*)(w + (e + y) * W_PITCH + lane * 4);
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      const float4 r4 = *(const float4*)&rows[r0 + x][e];
+      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        out[x][0] = fmaf(rv[y], v[y].x, out[x][0]);
+        out[x][1] = fmaf(rv[y], v[y].y, out[x][1]);
+        out[x][2] = fmaf(rv[y], v[y].z, out[x][2]);
+        out[x][3] = fmaf(rv[y], v[y].w, out[x][3]);
+      }
+    }
+  }
+}
+
+// acc[8][8] += sum_r a[r][8 ty ..] b[r][4 tx .. and 64 + 4 tx ..]: a thread's tile of a^T b
+template <int R>
 __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)[DD], float (*acc)[8]) {
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll 2
-  for (int r = 0; r < RB; ++r) {
+  for (int r = 0; r < R; ++r) {
     const float4 a0 = *(const float4*)&a[r][8 * ty], a1 = *(const float4*)&a[r][8 * ty + 4];
-    const float4 b0 = *(const float4*)&b[r][8 * tx], b1 = *(const float4*)&b[r][8 * tx + 4];
+    const float4 b0 = *(const float4*)&b[r][4 * tx], b1 = *(const float4*)&b[r][64 + 4 * tx];
     const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
     const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -786,134 +816,142 @@ __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)
       for (int x = 0; x < 8; ++x) acc[i][x] = fmaf(av[i], bv[x], acc[i][x]);
   }
 }
-__device__ __forceinline__ void store_outer(float* __restrict__ part, const float (*acc)[8]) {
+__device__ __forceinline__ void store_outer(float* __restrict__ part, const float (*acc)[8], float f) {
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float4* dst = (float4*)(part + (8 * ty + i) * DD + 8 * tx);
-    dst[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    dst[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    float* dst = part + (8 * ty + i) * DD + 4 * tx;
+    *(float4*)dst = make_float4(f * acc[i][0], f * acc[i][1], f * acc[i][2], f * acc[i][3]);
+    *(float4*)(dst + 64) = make_float4(f * acc[i][4], f * acc[i][5], f * acc[i][6], f * acc[i][7]);
   }
 }
+// four columns of a row as hi + lo bf16
+__device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo, int64_t at, const float* x) {
+  uint2 h, l;
+  split2(x[0], x[1], h.x, l.x);
+  split2(x[2], x[3], h.y, l.y);
+  *(uint2*)(hi + at) = h;
+  *(uint2*)(lo + at) = l;
+}
 
-// CTAs [0, kp / 8): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others, 8 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
+// CTAs [0, kp / 32): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
+// The others, 32 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
 // (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
-__global__ void __launch_bounds__(R_THREADS) tw_prepare_kernel(
+__global__ void __launch_bounds__(R_THREADS, 1) tw_prepare_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
     const float* __restrict__ W_Q, const float* __restrict__ W_K, const float* __restrict__ W_V,
     const float* __restrict__ dS, const float* __restrict__ H, float* __restrict__ Q, __nv_bfloat16* __restrict__ Uhi,
     __nv_bfloat16* __restrict__ Ulo, __nv_bfloat16* __restrict__ Hhi, __nv_bfloat16* __restrict__ Hlo,
     float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v) {
-  __shared__ float a[RB][DD], b[RB][DD], dots[R_THREADS / 32][RB];
-  const int warp = threadIdx.x / 32, col = warp * 16 + threadIdx.x % 16, h = threadIdx.x % 32 / 16;
-  const int groups = kp / RB;
-  float v[RB];
+  extern __shared__ __align__(16) float sm[];
+  float *w0 = sm, *w1 = sm + DD * W_PITCH;
+  float (*a)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*b)[DD] = a + RP;
+  constexpr int N = RP / 8;
+  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N, groups = kp / RP;
+  float v[N][4];
   if ((int)blockIdx.x < groups) {
-    const int j0 = blockIdx.x * RB;
-    load_block(a, P + (int64_t)j0 * DD, k - j0);
+    const int j0 = blockIdx.x * RP;
+    load_block<RP>(a, P + (int64_t)j0 * DD, k - j0);
+    load_weight(w0, W_Q);
+    load_weight_transposed(w1, W_K);
     __syncthreads();
-    rows_product<false>(a, W_Q, v);
+    rows_product<RP>(a, w0, v);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      if (r / (RB / 2) != h) continue;       // each half-warp keeps half of the rows
-      b[r][col] = v[r];
-      if (j0 + r < k) Q[(int64_t)(j0 + r) * DD + col] = v[r];
+    for (int x = 0; x < N; ++x) {
+      const float4 q = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
+      *(float4*)&b[r0 + x][lane * 4] = q;    // read back by this warp only
+      if (j0 + r0 + x < k) *(float4*)(Q + (int64_t)(j0 + r0 + x) * DD + lane * 4) = q;
     }
-    __syncthreads();
-    rows_product<true>(b, W_K, v);
+    __syncwarp();
+    rows_product<RP>(b, w1, v);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      if (r / (RB / 2) != h) continue;
-      const float x = v[r] * u_scale;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-      Uhi[(int64_t)(j0 + r) * DD + col] = hi;
-      Ulo[(int64_t)(j0 + r) * DD + col] = __float2bfloat16_rn(x - __bfloat162float(hi));
+    for (int x = 0; x < N; ++x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[x][i] *= u_scale;
+      store_split(Uhi, Ulo, (int64_t)(j0 + r0 + x) * DD + lane * 4, v[x]);
     }
     return;
   }
   const int part = blockIdx.x - groups, parts = gridDim.x - groups;
   float dwv[8][8] = {};
+  load_weight_transposed(w0, W_V);
   for (int64_t g = part; g < (int64_t)B * groups; g += parts) {
-    const int u = (int)(g / groups), j0 = (int)(g % groups) * RB;
+    const int u = (int)(g / groups), j0 = (int)(g % groups) * RP;
     const int have = off[u + 1] > off[u] ? k - j0 : 0;
-    const int64_t in = ((int64_t)u * k + j0) * DD, out = ((int64_t)u * kp + j0) * DD;
+    const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0 + r0;
     __syncthreads();
-    load_block(a, dS + in, have);
-    load_block(b, H + in, have);
+    load_block<RP>(a, dS + in, have);
+    load_block<RP>(b, H + in, have);
     __syncthreads();
-    rows_product<true>(a, W_V, v);
+    rows_product<RP>(a, w0, v);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
-      v[r] *= inv;
-      float dot = v[r] * b[r][col];
-      for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (threadIdx.x % 32 == 0) dots[warp][r] = dot;
-      if (r / (RB / 2) != h) continue;
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v[r]);
-      Hhi[out + r * DD + col] = hi;
-      Hlo[out + r * DD + col] = __float2bfloat16_rn(v[r] - __bfloat162float(hi));
+    for (int x = 0; x < N; ++x) {
+      const float4 hv = *(const float4*)&b[r0 + x][lane * 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[x][i] *= inv;
+      float dot = fmaf(v[x][0], hv.x, fmaf(v[x][1], hv.y, fmaf(v[x][2], hv.z, v[x][3] * hv.w)));
+      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) {
+        cj[row0 + x] = dot;
+        c2[row0 + x] = kLn2 * dot;
+      }
+      store_split(Hhi, Hlo, (row0 + x) * DD + lane * 4, v[x]);
     }
-    add_outer(b, a, dwv);
-    __syncthreads();
-    if (threadIdx.x < RB) {
-      float c = 0.f;
-      for (int w = 0; w < R_THREADS / 32; ++w) c += dots[w][threadIdx.x];
-      const int64_t row = (int64_t)u * kp + j0 + threadIdx.x;
-      cj[row] = c;
-      c2[row] = kLn2 * c;
-    }
+    add_outer<RP>(b, a, dwv);
   }
-  store_outer(part_v + (int64_t)part * DD * DD, dwv);
+  store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
 }
 
-// 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
+// 16 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
 // the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
-__global__ void __launch_bounds__(R_THREADS) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
-                                                               const float* __restrict__ P, const float* __restrict__ Q,
-                                                               const float* __restrict__ W_Q,
-                                                               const float* __restrict__ W_K, float* __restrict__ dP,
-                                                               float* __restrict__ part_qk) {
-  __shared__ float e[RB][DD], q[RB][DD], dq[RB][DD];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, col = warp * 16 + lane % 16, h = lane / 16;
-  float dwq[8][8] = {}, dwk[8][8] = {};
-  for (int j0 = blockIdx.x * RB; j0 < k; j0 += gridDim.x * RB) {
+__global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
+                                                                  const float* __restrict__ P,
+                                                                  const float* __restrict__ Q,
+                                                                  const float* __restrict__ W_Q,
+                                                                  const float* __restrict__ W_K, float* __restrict__ dP,
+                                                                  float* __restrict__ part_qk) {
+  extern __shared__ __align__(16) float sm[];
+  float *w0 = sm, *w1 = sm + DD * W_PITCH;
+  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW;
+  constexpr int N = RW / 8;
+  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N;
+  float dwq[8][8] = {}, dwk[8][8] = {}, v[N][4];
+  load_weight(w0, W_K);
+  load_weight_transposed(w1, W_Q);
+  for (int j0 = blockIdx.x * RW; j0 < k; j0 += gridDim.x * RW) {
     __syncthreads();
-    for (int r = warp; r < RB; r += R_THREADS / 32) {
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j0 + r < k) {
-        const float* src = Epart + (int64_t)(j0 + r) * DD + lane * 4;
+      if (j0 + r0 + x < k) {
+        const float* src = Epart + (int64_t)(j0 + r0 + x) * DD + lane * 4;
 #pragma unroll 8
         for (int g = 0; g < G; ++g) {
-          const float4 x = *(const float4*)(src + (int64_t)g * k * DD);
-          s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+          const float4 y = *(const float4*)(src + (int64_t)g * k * DD);
+          s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
         }
       }
-      *(float4*)&e[r][lane * 4] = s;
+      *(float4*)&e[r0 + x][lane * 4] = s;
     }
-    load_block(q, Q + (int64_t)j0 * DD, k - j0);
+    load_block<RW>(q, Q + (int64_t)j0 * DD, k - j0);
     __syncthreads();
-    add_outer(e, q, dwk);
-    float v[RB];
-    rows_product<false>(e, W_K, v);
+    add_outer<RW>(e, q, dwk);
+    rows_product<RW>(e, w0, v);
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-      if (r / (RB / 2) == h) dq[r][col] = v[r] * rs;
-    __syncthreads();                         // and q is no longer read: the rows of P replace it
-    load_block(q, P + (int64_t)j0 * DD, k - j0);
-    rows_product<true>(dq, W_Q, v);
+    for (int x = 0; x < N; ++x)
+      *(float4*)&dq[r0 + x][lane * 4] = make_float4(v[x][0] * rs, v[x][1] * rs, v[x][2] * rs, v[x][3] * rs);
+    __syncthreads();                         // q is no longer read: the rows of P replace it
+    load_block<RW>(q, P + (int64_t)j0 * DD, k - j0);
+    rows_product<RW>(dq, w1, v);
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
-      if (r / (RB / 2) == h && j0 + r < k) dP[(int64_t)(j0 + r) * DD + col] = v[r];
+    for (int x = 0; x < N; ++x)
+      if (j0 + r0 + x < k)
+        *(float4*)(dP + (int64_t)(j0 + r0 + x) * DD + lane * 4) = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
     __syncthreads();
-    add_outer(q, dq, dwq);
+    add_outer<RW>(q, dq, dwq);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int x = 0; x < 8; ++x) dwk[i][x] *= rs;
-  store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq);
-  store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk);
+  store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq, 1.f);
+  store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk, rs);
 }
 
 // dW_V = i times the sum of its parts, dW_Q and dW_K the sums of theirs: a CTA per 128 values, its
@@ -953,8 +991,11 @@ Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
 // CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again)
-int value_parts(int B, int k) { return std::min(B * (padded_k(k) / RB), 128); }
-int weight_parts(int k) { return std::min((k + RB - 1) / RB, 64); }
+int value_parts(int B, int k) {
+  const int groups = padded_k(k) / RP;
+  return (int)std::min<int64_t>((int64_t)B * groups, std::max(32, device_info().sm_count - groups));
+}
+int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
 
 sa_status map_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_rows) {
@@ -983,17 +1024,19 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
 }
 
 sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st) {
-  static unsigned long long done_s = 0, done_e = 0, done_x = 0;
+  static unsigned long long done_s = 0, done_e = 0, done_x = 0, done_p = 0, done_w = 0;
   static std::mutex mu;
   set_smem_limit_once((const void*)tw_lse_kernel, S_SMEM, &done_s, mu);
   set_smem_limit_once((const void*)tw_e_kernel, E_SMEM, &done_e, mu);
   set_smem_limit_once((const void*)tw_dx_kernel, X_SMEM, &done_x, mu);
+  set_smem_limit_once((const void*)tw_prepare_kernel, PREP_SMEM, &done_p, mu);
+  set_smem_limit_once((const void*)tw_weights_kernel, WEIGHTS_SMEM, &done_w, mu);
   const int kp = padded_k(a.k), slices = kp / TILE, n_v = value_parts(a.B, a.k), n_qk = weight_parts(a.k);
   const float inv = 1.f / (1.f + a.eps);                // m = 1 for a user with events
   const float rs = 1.f / sqrtf((float)a.d);
   sa_status s;
   SA_TIMED("tw_prepare_kernel", st,
-           (tw_prepare_kernel<<<kp / RB + n_v, R_THREADS, 0, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
+           (tw_prepare_kernel<<<kp / RP + n_v, R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
                                                                    a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi, w.Ulo,
                                                                    w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
   if (a.n_total > 0) {
@@ -1020,7 +1063,7 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
              (tw_e_kernel<<<w.chE.G * slices, E_THREADS, E_SMEM, st>>>(tmX, tmU, tmUlo, tmH, tmHlo, ep)));
   }
   SA_TIMED("tw_weights_kernel", st,
-           (tw_weights_kernel<<<n_qk, R_THREADS, 0, st>>>(a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q, a.W_K, a.dP,
+           (tw_weights_kernel<<<n_qk, R_THREADS, WEIGHTS_SMEM, st>>>(a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q, a.W_K, a.dP,
                                                           w.part_qk)));
   SA_TIMED("tw_sum_kernel", st,
            (tw_sum_kernel<<<3 * DD, R_THREADS, 0, st>>>(w.part_v, n_v, inv, w.part_qk, n_qk, a.dW_V, a.dW_Q, a.dW_K)));

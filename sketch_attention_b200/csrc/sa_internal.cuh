@@ -137,8 +137,8 @@ struct TokenwiseBwdWork {
   __nv_bfloat16 *Hhi, *Hlo;   // [B, kp, d] dH as hi + lo
   float *c, *c2;         // [B, kp] dH . H, and ln2 times it
   float* lse2;           // [B, kp] log2 of the rows' sums of 2^z
-  float2* stat_user;     // [B, 2, kp] (max, sum) of users inside one chunk
-  float2* stat_slot;     // [G, 2, 2, kp] of the pieces of users that span chunks
+  float2* stat_user;     // [B, 4, kp] (max, sum) of users inside one chunk
+  float2* stat_slot;     // [G, 2, 4, kp] of the pieces of users that span chunks
   float* Epart;          // [G, k, d]
   float* part_v;         // [CTAs, d, d] parts of sum H^T dS
   float* part_qk;        // [CTAs, 2, d, d] parts of dW_Q and dW_K

@@ -57,9 +57,13 @@ __device__ __forceinline__ void for_each_tile(const int64_t* off, int B, const C
   }
 }
 
-__device__ __forceinline__ uint64_t kmajor(uint32_t base, int ks) {
-  return smem_desc(base + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024, SWZ_128B);
-}
+// Descriptors of an operand's 16-deep K steps: a base, computed once per stage, plus a constant
+// (added to the address field, which does not overflow).  One thread issues all MMAs: with a
+// descriptor built for each, an MMA took it 90 to 110 clocks, the tensor core 64.
+__device__ __forceinline__ uint64_t kmajor(uint32_t addr) { return smem_desc(addr, 16, 1024, SWZ_128B); }
+__device__ constexpr uint64_t kstep(int ks) { return ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4; }
+__device__ __forceinline__ uint64_t mnmajor(uint32_t addr) { return smem_desc(addr, 16384, 1024, SWZ_128B); }
+__device__ constexpr uint64_t mnstep(int ks) { return ks * 2048 >> 4; }
 
 // x = hi + lo as bf16 pairs
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -85,7 +89,10 @@ constexpr uint32_t S_OFF_U = 0;                                  // U hi, U lo
 constexpr uint32_t S_OFF_X = 2 * XT_BYTES;
 constexpr uint32_t S_OFF_BAR = S_OFF_X + S_NXS * XT_BYTES;
 constexpr uint32_t S_SMEM = S_OFF_BAR + 256 + 1024;
-constexpr int S_THREADS = 320;               // warp 0 TMA, 1 MMA, 2-9 two threads per prototype
+// warp 0 TMA, 1 MMA, 2-9 the even tiles and 10-17 the odd ones, two threads per prototype: the teams
+// are in different phases, so that the exponentials of one fill the other's waits (one team: 1810
+// clocks a tile, 1024 of them exponentials)
+constexpr int S_THREADS = 576, S_PARTS = 4;  // (max, sum) pairs per prototype: team, column half
 
 struct SBars {
   uint64_t u_full, x_full[S_NXS], x_empty[S_NXS], z_full[2], z_empty[2], mma_done;
@@ -98,8 +105,8 @@ struct SParams {
   int B;
   Chunking ch;
   int slices, kp;
-  float2* user;          // [B, 2, kp] (max, sum) of users inside one chunk, by column half
-  float2* slot;          // [G, 2, 2, kp] of the pieces of users that span chunks
+  float2* user;          // [B, S_PARTS, kp] (max, sum) of users inside one chunk
+  float2* slot;          // [G, 2, S_PARTS, kp] of the pieces of users that span chunks
   int* err;
 };
 
@@ -151,18 +158,19 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     }
   } else if (warp == 1 && lane == 0) {
     const uint32_t id = idesc_bf16(128, 128, false, false);
-    const uint32_t ua = smem_u32(smem + S_OFF_U);
+    const uint64_t du = kmajor(smem_u32(smem + S_OFF_U)), dulo = kmajor(smem_u32(smem + S_OFF_U + XT_BYTES));
     if (mbar_wait(&bars->u_full, 0, abort, p.err))
       for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
         const int s = t % S_NXS, b = t & 1;
         if (!mbar_wait(&bars->x_full[s], (t / S_NXS) & 1, abort, p.err)) return false;
         if (t >= 2 && !mbar_wait(&bars->z_empty[b], ((t >> 1) - 1) & 1, abort, p.err)) return false;
         tc_fence_after();
-        const uint32_t xa = smem_u32(smem + S_OFF_X + s * XT_BYTES);
+        const uint64_t dx = kmajor(smem_u32(smem + S_OFF_X + s * XT_BYTES));
+        const uint32_t z = tmem + 128 * b;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss(tmem + 128 * b, kmajor(ua, ks), kmajor(xa, ks), id, ks > 0);
+        for (int ks = 0; ks < 8; ++ks) mma_ss(z, du + kstep(ks), dx + kstep(ks), id, ks > 0);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss(tmem + 128 * b, kmajor(ua + XT_BYTES, ks), kmajor(xa, ks), id, 1u);
+        for (int ks = 0; ks < 8; ++ks) mma_ss(z, dulo + kstep(ks), dx + kstep(ks), id, 1u);
         mma_commit(&bars->z_full[b]);
         mma_commit(&bars->x_empty[s]);
         return true;
@@ -170,47 +178,50 @@ __global__ void __launch_bounds__(S_THREADS, 1)
     mma_commit(&bars->mma_done);
     mbar_wait_bounded(&bars->mma_done, 0);
   } else if (warp >= 2) {
-    const int q = warp % 4, h = (warp - 2) / 4;          // column half: events 64 h .. 64 h + 63 of a tile
-    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    // column half h: events 64 h .. 64 h + 63 of a tile
+    const int q = warp % 4, team = (warp - 2) / 8, h = (warp - 2) / 4 % 2;
+    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + 128 * team + 64 * h;
     const int j = sl * TILE + q * 32 + lane;
     const int64_t cb = (int64_t)g * p.ch.T, ce = min(cb + p.ch.T, p.ch.n_total);
     float m = -INFINITY, sum = 0.f;
     for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int u, int64_t tb, int64_t pe, bool first, bool last) {
-      const int b = t & 1;
       if (first) { m = -INFINITY; sum = 0.f; }
-      if (!mbar_wait(&bars->z_full[b], (t >> 1) & 1, abort, p.err)) return false;
-      tc_fence_after();
-      float z[64];
-      tmem_ld32(tmem + lane_addr + 128 * b + 64 * h, z);
-      tmem_ld32(tmem + lane_addr + 128 * b + 64 * h + 32, z + 32);
-      wait_ld<64>(z);
-      tc_fence_before();
-      mbar_arrive(&bars->z_empty[b]);
       const int nv = (int)min(pe - tb - 64 * h, (int64_t)64);   // events of this half that are the user's
-      if (nv > 0) {
-        if (nv < 64) {
+      if ((t & 1) == team) {
+        if (!mbar_wait(&bars->z_full[team], (t >> 1) & 1, abort, p.err)) return false;
+        tc_fence_after();
+        float z[64];
+        tmem_ld32(at, z);
+        tmem_ld32(at + 32, z + 32);
+        wait_ld<64>(z);
+        tc_fence_before();
+        mbar_arrive(&bars->z_empty[team]);
+        if (nv > 0) {
+          if (nv < 64) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i >= nv) z[i] = -INFINITY;
+            for (int i = 0; i < 64; ++i)
+              if (i >= nv) z[i] = -INFINITY;
+          }
+          float mx[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+          for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
+          const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          const float2 nm = make_float2(-mn, -mn);
+          float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nm);
+            s2[(i >> 1) & 1] = __fadd2_rn(s2[(i >> 1) & 1], make_float2(ex2(e.x), ex2(e.y)));
+          }
+          sum = fmaf(sum, ex2(m - mn), (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
+          m = mn;
         }
-        float mx[4] = {z[0], z[1], z[2], z[3]};
-#pragma unroll
-        for (int i = 4; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], z[i]);
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-        const float2 nm = make_float2(-mn, -mn);
-        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nm);
-          s2[(i >> 1) & 1] = __fadd2_rn(s2[(i >> 1) & 1], make_float2(ex2(e.x), ex2(e.y)));
-        }
-        sum = fmaf(sum, ex2(m - mn), (s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
-        m = mn;
       }
       if (last) {
         const int dest = piece_dest(p.off[u], p.off[u + 1], cb, ce);
-        float2* out = dest == DEST_USER ? p.user + (int64_t)u * 2 * p.kp : p.slot + ((int64_t)g * 2 + dest) * 2 * p.kp;
-        out[(int64_t)h * p.kp + j] = make_float2(m, sum);
+        float2* out = dest == DEST_USER ? p.user + (int64_t)u * S_PARTS * p.kp
+                                        : p.slot + ((int64_t)g * 2 + dest) * S_PARTS * p.kp;
+        out[(int64_t)(2 * team + h) * p.kp + j] = make_float2(m, sum);
       }
       return true;
     });
@@ -237,10 +248,12 @@ __global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __re
       const int64_t gf = ub / ch.T, gl = (ue - 1) / ch.T;
       float m = -INFINITY, s = 0.f;
       for (int64_t g = gf; g <= gl; ++g) {
-        const float2* p = gf == gl ? user + (int64_t)u * 2 * kp : slot + (g * 2 + (g == gf ? 1 : 0)) * 2 * kp;
-        for (int h = 0; h < 2; ++h) {
+        const float2* p = gf == gl ? user + (int64_t)u * S_PARTS * kp
+                                   : slot + (g * 2 + (g == gf ? 1 : 0)) * S_PARTS * kp;
+#pragma unroll
+        for (int h = 0; h < S_PARTS; ++h) {
           const float2 v = p[(int64_t)h * kp + j];
-          if (v.x == -INFINITY && v.y == 0.f) continue;  // a half without events
+          if (v.x == -INFINITY && v.y == 0.f) continue;  // a part without events
           const float mn = fmaxf(m, v.x);
           s = s * exp2f(m - mn) + v.y * exp2f(v.x - mn);
           m = mn;
@@ -342,18 +355,18 @@ __global__ void __launch_bounds__(E_THREADS, 1)
   } else if (warp == 1 && lane == 0) {
     const uint32_t id_zg = idesc_bf16(128, 128, false, false);
     const uint32_t id_e = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
-    const uint32_t ua = smem_u32(smem + E_OFF_U);
+    const uint64_t du = kmajor(smem_u32(smem + E_OFF_U));
     auto x_at = [&](int t) { return smem_u32(smem + E_OFF_X + (t % E_NXS) * XT_BYTES); };
     // E += dZ X of tile t (afresh after every drain)
     auto emma = [&](int t) -> bool {
       if (!mbar_wait(&bars->dz_full, t & 1, abort, p.err)) return false;
       tc_fence_after();
-      const uint32_t xa = x_at(t);
+      const uint64_t dx = mnmajor(x_at(t));
+      const uint32_t kept = t % kDrain != 0 ? 1u : 0u;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const uint64_t bx = smem_desc(xa + ks * 2048, 16384, 1024, SWZ_128B);
-        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, bx, id_e, (t % kDrain != 0 || ks > 0) ? 1u : 0u);
-        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, bx, id_e, 1u);
+        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, dx + mnstep(ks), id_e, ks > 0 ? 1u : kept);
+        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, dx + mnstep(ks), id_e, 1u);
       }
       mma_commit(&bars->e_done);
       mma_commit(&bars->x_empty[t % E_NXS]);
@@ -366,12 +379,12 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         if (!mbar_wait(&bars->x_full[t % E_NXS], (t / E_NXS) & 1, abort, p.err)) return false;
         if (t > 0 && !mbar_wait(&bars->zg_empty, (t - 1) & 1, abort, p.err)) return false;
         tc_fence_after();
-        const uint32_t xa = x_at(t);
+        const uint64_t dx = kmajor(x_at(t));
 #pragma unroll
         for (int o = 0; o < 4; ++o)                      // Z = (U hi + U lo) X^T, G = (dH hi + dH lo) X^T
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), kmajor(ua + o * XT_BYTES, ks), kmajor(xa, ks), id_zg,
+            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), id_zg,
                    (o & 1) || ks > 0);
         mma_commit(&bars->zg_full);
         if (last) mma_commit(&bars->h_empty);
@@ -478,7 +491,7 @@ constexpr uint32_t X_OFF_CH = 2 * XT_BYTES;
 constexpr uint32_t X_OFF_ROW = X_OFF_CH + X_NCS * CH_BYTES;      // [X_NCS][lse2 64 | ln2 c 64]
 constexpr uint32_t X_OFF_BAR = X_OFF_ROW + X_NCS * 2 * KC * 4;
 constexpr uint32_t X_SMEM = X_OFF_BAR + 256 + 1024;
-constexpr int X_THREADS = 576;               // warp 0 TMA, 1 MMA, 2-9 tile 0 and 10-17 tile 1, two threads per token
+constexpr int X_THREADS = 576;               // warp 0 TMA, 1 MMA, 2-17 four threads per token, both tiles in turn
 // TMEM columns of tile i: [Z|G] at 128 i, later A and ln2 dZ as bf16 pairs in the columns of Z;
 // dX at 256 + 128 i
 constexpr uint32_t X_TM_ZG = 0, X_TM_Q = 256;
@@ -539,7 +552,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       mbar_init(&bars->x_full[i], 1);
       mbar_init(&bars->x_empty[i], 1);
       mbar_init(&bars->zg_full[i], 1);
-      mbar_init(&bars->aa_full[i], 256);
+      mbar_init(&bars->aa_full[i], 512);
       mbar_init(&bars->q_full[i], 1);
     }
     for (int s = 0; s < X_NCS; ++s) { mbar_init(&bars->c_full[s], 1); mbar_init(&bars->c_empty[s], 1); }
@@ -606,14 +619,14 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       const int s = cc % X_NCS;
       if (!mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) return false;
       tc_fence_after();
-      const uint32_t xa = smem_u32(smem + X_OFF_X + i * XT_BYTES), cb = smem_u32(smem + X_OFF_CH + s * CH_BYTES);
+      const uint64_t dx = kmajor(smem_u32(smem + X_OFF_X + i * XT_BYTES));
+      const uint64_t dc = kmajor(smem_u32(smem + X_OFF_CH + s * CH_BYTES));
+      const uint32_t zg = tmem + X_TM_ZG + 128 * i;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_ss(zg, dx + kstep(ks), dc + kstep(ks), id_zg, ks > 0);
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
-        mma_ss(tmem + X_TM_ZG + 128 * i, kmajor(xa, ks), kmajor(cb, ks), id_zg, ks > 0);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        mma_ss(tmem + X_TM_ZG + 128 * i, kmajor(xa, ks),
-               smem_desc(cb + 32768 + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024, SWZ_128B), id_lo, 1u);
+        mma_ss(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_lo, 1u);
       mma_commit(&bars->zg_full[i]);
       if (last) mma_commit(&bars->x_empty[i]);
       return true;
@@ -623,14 +636,14 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       if (!mbar_wait(&bars->aa_full[i], at[i] & 1, abort, p.err)) return false;
       ++at[i];
       tc_fence_after();
-      const uint32_t cb = smem_u32(smem + X_OFF_CH + (cc % X_NCS) * CH_BYTES);
+      const uint64_t dc = mnmajor(smem_u32(smem + X_OFF_CH + (cc % X_NCS) * CH_BYTES));
+      const uint32_t q = tmem + X_TM_Q + 128 * i, kept = first ? 0u : 1u;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) {
-        // prototypes 16 ks ..: written by the threads of half ks / 2, A then dZ, 16 columns each
-        const uint32_t a = tmem + X_TM_ZG + 128 * i + 32 * (ks >> 1) + 8 * (ks & 1);
-        mma_ts(tmem + X_TM_Q + 128 * i, a, smem_desc(cb + 8192 + ks * 2048, 16384, 1024, SWZ_128B), id_q,
-               (first && ks == 0) ? 0u : 1u);
-        mma_ts(tmem + X_TM_Q + 128 * i, a + 16, smem_desc(cb + ks * 2048, 16384, 1024, SWZ_128B), id_q, 1u);
+        // prototypes 16 ks ..: written by the threads of quarter ks, A then dZ, 8 columns each
+        const uint32_t a = tmem + X_TM_ZG + 128 * i + 16 * ks;
+        mma_ts(q, a, dc + (8192 >> 4) + mnstep(ks), id_q, ks > 0 ? 1u : kept);
+        mma_ts(q, a + 8, dc + mnstep(ks), id_q, 1u);
       }
       if (frees) mma_commit(&bars->c_empty[cc % X_NCS]);
       if (last) mma_commit(&bars->q_full[i]);
@@ -657,72 +670,72 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     mma_commit(&bars->mma_done);
     mbar_wait_bounded(&bars->mma_done, 0);
   } else if (warp >= 2) {
-    // ------------------------------------------------------------ two threads per token
-    const int q = warp % 4, i = (warp - 2) / 8, h = ((warp - 2) / 4) & 1;
+    // ------------------------------------------------------------ four threads per token
+    const int q = warp % 4, w = (warp - 2) / 4;          // prototypes 16 w .. 16 w + 15 of a stage
     const int row = q * 32 + lane;
-    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
-    const uint32_t own = tmem + lane_addr + X_TM_ZG + 128 * i + 32 * h;   // Z of prototypes 32 h .. 32 h + 31
+    const uint32_t lane_addr = tmem + ((uint32_t)(q * 32) << 16);
     const float2 ln2v = make_float2(kLn2, kLn2);
-    int cc = 0, a = 0, t = 0;                // stage counter; stages and units of this thread's tile
+    int cc = 0, a[2] = {0, 0}, t[2] = {0, 0};            // stage counter; stages and units per tile
     bool ok = true;
     for (Units un(p, g); ok && !un.done(); un.next()) {
-      if (i == 1 && !un.two()) {
-        cc += nch;
-        continue;
-      }
-      for (int c = 0; c < nch; ++c, ++cc, ++a) {
+      const int n_tiles = un.two() ? 2 : 1;
+      for (int c = 0; ok && c < nch; ++c, ++cc) {
         const int s = cc % X_NCS;
-        if (!mbar_wait(&bars->zg_full[i], a & 1, abort, p.err) ||
-            !mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) { ok = false; break; }
-        tc_fence_after();
-        float z[32], gv[32];
-        tmem_ld32(own, z);
-        tmem_ld32(own + 64, gv);
-        wait_ld<32>(z);
-        wait_ld<32>(gv);
-        const float4* l4 = (const float4*)(smem + X_OFF_ROW + s * 2 * KC * 4) + 8 * h;
+        const float4* l4 = (const float4*)(smem + X_OFF_ROW + s * 2 * KC * 4) + 4 * w;
         const float4* c4 = l4 + KC / 4;
-        uint32_t pk[32];                     // A in 0..15, ln2 dZ in 16..31 (even prototype low)
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-          const float4 l = l4[b], cv = c4[b];
-          const float2 lp[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
-          const float2 cp[2] = {make_float2(-cv.x, -cv.y), make_float2(-cv.z, -cv.w)};
+        for (int i = 0; i < 2; ++i) {
+          if (i >= n_tiles) break;
+          const uint32_t own = lane_addr + X_TM_ZG + 128 * i + 16 * w;
+          if (!mbar_wait(&bars->zg_full[i], a[i] & 1, abort, p.err) ||
+              !mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) { ok = false; break; }
+          ++a[i];
+          tc_fence_after();
+          float z[16], gv[16];
+          tmem_ld16(own, z);
+          tmem_ld16(own + 64, gv);
+          wait_ld<16>(z);
+          wait_ld<16>(gv);
+          uint32_t pk[16];                   // A in 0..7, ln2 dZ in 8..15 (even prototype low)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int j = 4 * b + 2 * x;
-            const float2 e = __fadd2_rn(make_float2(z[j], z[j + 1]), lp[x]);
-            const float2 A = make_float2(ex2(e.x), ex2(e.y));
-            const float2 dz = __fmul2_rn(A, __ffma2_rn(make_float2(gv[j], gv[j + 1]), ln2v, cp[x]));
-            pk[j / 2] = pack_bf16x2(A.x, A.y);
-            pk[16 + j / 2] = pack_bf16x2(dz.x, dz.y);
+          for (int b = 0; b < 4; ++b) {
+            const float4 l = l4[b], cv = c4[b];
+            const float2 lp[2] = {make_float2(-l.x, -l.y), make_float2(-l.z, -l.w)};
+            const float2 cp[2] = {make_float2(-cv.x, -cv.y), make_float2(-cv.z, -cv.w)};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int j = 4 * b + 2 * x;
+              const float2 e = __fadd2_rn(make_float2(z[j], z[j + 1]), lp[x]);
+              const float2 A = make_float2(ex2(e.x), ex2(e.y));
+              const float2 dz = __fmul2_rn(A, __ffma2_rn(make_float2(gv[j], gv[j + 1]), ln2v, cp[x]));
+              pk[j / 2] = pack_bf16x2(A.x, A.y);
+              pk[8 + j / 2] = pack_bf16x2(dz.x, dz.y);
+            }
           }
+          tmem_st16(own, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->aa_full[i]);
         }
-        tmem_st32(own, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->aa_full[i]);
       }
-      if (!ok) break;
-      // this thread's 64 columns of the token's dX
-      if (!mbar_wait(&bars->q_full[i], t & 1, abort, p.err)) { ok = false; break; }
-      tc_fence_after();
-      const int64_t r = un.tb + i * TILE + row;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      // this thread's 32 columns of its token's dX, in both tiles
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        if (!mbar_wait(&bars->q_full[i], t[i] & 1, abort, p.err)) { ok = false; break; }
+        ++t[i];
+        tc_fence_after();
+        const int64_t r = un.tb + i * TILE + row;
         float v[32];
-        tmem_ld32(tmem + lane_addr + X_TM_Q + 128 * i + 64 * h + 32 * b, v);
+        tmem_ld32(lane_addr + X_TM_Q + 128 * i + 32 * w, v);
         wait_ld<32>(v);
+        tc_fence_before();                   // read before this thread's next arrival at aa_full
         if (r < un.pe) {
-          uint4* dst = (uint4*)(p.dX + r * DD + 64 * h + 32 * b);
+          uint4* dst = (uint4*)(p.dX + r * DD + 32 * w);
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             dst[x] = make_uint4(pack_bf16x2(v[8 * x], v[8 * x + 1]), pack_bf16x2(v[8 * x + 2], v[8 * x + 3]),
                                 pack_bf16x2(v[8 * x + 4], v[8 * x + 5]), pack_bf16x2(v[8 * x + 6], v[8 * x + 7]));
         }
       }
-      tc_fence_before();                     // read before this thread's next arrival at aa_full
-      ++t;
     }
   }
 
@@ -1014,8 +1027,8 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
   for (__nv_bfloat16** p : {&v.Uhi, &v.Ulo}) *p = c.take<__nv_bfloat16>(kp * d);
   for (__nv_bfloat16** p : {&v.Hhi, &v.Hlo}) *p = c.take<__nv_bfloat16>((size_t)B * kp * d);
   for (float** p : {&v.c, &v.c2, &v.lse2}) *p = c.take<float>((size_t)B * kp);
-  v.stat_user = c.take<float2>((size_t)B * 2 * kp);
-  v.stat_slot = c.take<float2>(G * 4 * kp);
+  v.stat_user = c.take<float2>((size_t)B * S_PARTS * kp);
+  v.stat_slot = c.take<float2>(G * 2 * S_PARTS * kp);
   v.Epart = c.take<float>(G * kd);
   v.part_v = c.take<float>(value_parts(B, k) * dd);
   v.part_qk = c.take<float>(weight_parts(k) * 2 * dd);

@@ -58,8 +58,15 @@ __device__ __forceinline__ void for_each_tile(const int64_t* off, int B, const C
 }
 
 // Descriptors of an operand's 16-deep K steps: a base, computed once per stage, plus a constant
-// (added to the address field, which does not overflow).  One thread issues all MMAs: with a
-// descriptor built for each, an MMA took it 90 to 110 clocks, the tensor core 64.
+// (added to the address field, which does not overflow).
+//
+// Every kernel has two threads that issue MMAs.  The tensor core takes a 128 x 128 x 16 product every
+// 64 clocks and queues only a few, so a thread that issues a stage's products, waits for the next
+// stage's barriers and loops (500 clocks even when all are ready) leaves it idle meanwhile: one
+// thread for 16 products a tile measured 1665 clocks instead of 1024.  The two take turns, a stage
+// each, waiting for their own barriers during the other's turn.  Without turns they issue at the same
+// time and then wait at the same time: both stages finish late, and the tensor core idles while the
+// warps work on both (dX: 4130 clocks per two stages of 1408).
 __device__ __forceinline__ uint64_t kmajor(uint32_t addr) { return smem_desc(addr, 16, 1024, SWZ_128B); }
 __device__ constexpr uint64_t kstep(int ks) { return ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4; }
 __device__ __forceinline__ uint64_t mnmajor(uint32_t addr) { return smem_desc(addr, 16384, 1024, SWZ_128B); }
@@ -78,6 +85,16 @@ __device__ __forceinline__ void wait_ld(float* v) {
   for (int i = 0; i < N; i += 16) tmem_wait_ld16(v + i);
 }
 
+// The turns of the two issuing threads: thread 0 goes first, then they alternate (n: turns taken so
+// far).  A turn ends when its products are issued, not when they are complete.
+struct Turns {
+  uint64_t bar[2];
+};
+__device__ __forceinline__ bool turn_wait(Turns* t, int i, int n, volatile int* abort, int* err) {
+  return mbar_wait(&t->bar[i], i == 0 ? (n & 1) ^ 1 : n & 1, abort, err);
+}
+__device__ __forceinline__ void turn_pass(Turns* t, int i) { mbar_arrive(&t->bar[1 - i]); }
+
 __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row) {
   tma_load_2d(dst, map, bar, 0, row);
   tma_load_2d(dst + XT_BYTES / 2, map, bar, 64, row);
@@ -89,13 +106,14 @@ constexpr uint32_t S_OFF_U = 0;                                  // U hi, U lo
 constexpr uint32_t S_OFF_X = 2 * XT_BYTES;
 constexpr uint32_t S_OFF_BAR = S_OFF_X + S_NXS * XT_BYTES;
 constexpr uint32_t S_SMEM = S_OFF_BAR + 256 + 1024;
-// warp 0 TMA, 1 MMA, 2-9 the even tiles and 10-17 the odd ones, two threads per prototype: the teams
-// are in different phases, so that the exponentials of one fill the other's waits (one team: 1810
-// clocks a tile, 1024 of them exponentials)
-constexpr int S_THREADS = 576, S_PARTS = 4;  // (max, sum) pairs per prototype: team, column half
+// warp 0 TMA, 1 and 18 the MMAs of the even and the odd tiles, 2-9 the even tiles' statistics and
+// 10-17 the odd ones', two threads per prototype: the teams are in different phases, so that the
+// exponentials of one (1024 clocks a tile) fill the other's waits
+constexpr int S_THREADS = 608, S_PARTS = 4;  // (max, sum) pairs per prototype: team, column half
 
 struct SBars {
-  uint64_t u_full, x_full[S_NXS], x_empty[S_NXS], z_full[2], z_empty[2], mma_done;
+  uint64_t u_full, x_full[S_NXS], x_empty[S_NXS], z_full[2], z_empty[2], mma_done[2];
+  Turns turns;
   uint32_t tmem_base;
   int abort;
 };
@@ -123,8 +141,12 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   if (threadIdx.x == 0) {
     mbar_init(&bars->u_full, 1);
     for (int s = 0; s < S_NXS; ++s) { mbar_init(&bars->x_full[s], 1); mbar_init(&bars->x_empty[s], 1); }
-    for (int b = 0; b < 2; ++b) { mbar_init(&bars->z_full[b], 1); mbar_init(&bars->z_empty[b], 256); }
-    mbar_init(&bars->mma_done, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->z_full[b], 1);
+      mbar_init(&bars->z_empty[b], 256);
+      mbar_init(&bars->mma_done[b], 1);
+      mbar_init(&bars->turns.bar[b], 1);
+    }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -156,28 +178,33 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       for (int t = std::max(0, issued - S_NXS); t < issued; ++t)
         mbar_wait_bounded(&bars->x_full[t % S_NXS], (t / S_NXS) & 1);
     }
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t id = idesc_bf16(128, 128, false, false);
+  } else if (warp == 1 || warp == 18) {
+    const int b = warp == 18;                // the parity of this thread's tiles
+    const uint32_t id = idesc_bf16(128, 128, false, false), z = tmem + 128 * b;
     const uint64_t du = kmajor(smem_u32(smem + S_OFF_U)), dulo = kmajor(smem_u32(smem + S_OFF_U + XT_BYTES));
-    if (mbar_wait(&bars->u_full, 0, abort, p.err))
-      for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
-        const int s = t % S_NXS, b = t & 1;
-        if (!mbar_wait(&bars->x_full[s], (t / S_NXS) & 1, abort, p.err)) return false;
-        if (t >= 2 && !mbar_wait(&bars->z_empty[b], ((t >> 1) - 1) & 1, abort, p.err)) return false;
-        tc_fence_after();
-        const uint64_t dx = kmajor(smem_u32(smem + S_OFF_X + s * XT_BYTES));
-        const uint32_t z = tmem + 128 * b;
+    if (lane == 0) {
+      if (mbar_wait(&bars->u_full, 0, abort, p.err))
+        for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
+          if ((t & 1) != b) return true;
+          const int s = t % S_NXS;
+          if (!mbar_wait(&bars->x_full[s], (t / S_NXS) & 1, abort, p.err)) return false;
+          if (t >= 2 && !mbar_wait(&bars->z_empty[b], ((t >> 1) - 1) & 1, abort, p.err)) return false;
+          if (!turn_wait(&bars->turns, b, t >> 1, abort, p.err)) return false;
+          tc_fence_after();
+          const uint64_t dx = kmajor(smem_u32(smem + S_OFF_X + s * XT_BYTES));
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss(z, du + kstep(ks), dx + kstep(ks), id, ks > 0);
+          for (int ks = 0; ks < 8; ++ks) mma_ss(z, du + kstep(ks), dx + kstep(ks), id, ks > 0);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss(z, dulo + kstep(ks), dx + kstep(ks), id, 1u);
-        mma_commit(&bars->z_full[b]);
-        mma_commit(&bars->x_empty[s]);
-        return true;
-      });
-    mma_commit(&bars->mma_done);
-    mbar_wait_bounded(&bars->mma_done, 0);
-  } else if (warp >= 2) {
+          for (int ks = 0; ks < 8; ++ks) mma_ss(z, dulo + kstep(ks), dx + kstep(ks), id, 1u);
+          turn_pass(&bars->turns, b);
+          mma_commit(&bars->z_full[b]);
+          mma_commit(&bars->x_empty[s]);
+          return true;
+        });
+      mma_commit(&bars->mma_done[b]);
+      mbar_wait_bounded(&bars->mma_done[b], 0);
+    }
+  } else if (warp >= 2 && warp < 18) {
     // column half h: events 64 h .. 64 h + 63 of a tile
     const int q = warp % 4, team = (warp - 2) / 8, h = (warp - 2) / 4 % 2;
     const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + 128 * team + 64 * h;
@@ -271,11 +298,11 @@ constexpr uint32_t E_OFF_U = 0;                                  // U hi, U lo, 
 constexpr uint32_t E_OFF_X = 4 * XT_BYTES;
 constexpr uint32_t E_OFF_BAR = E_OFF_X + E_NXS * XT_BYTES;
 constexpr uint32_t E_SMEM = E_OFF_BAR + 256 + 1024;
-constexpr int E_THREADS = 320;               // warp 0 TMA, 1 MMA, 2-9 two threads per prototype
+constexpr int E_THREADS = 608;               // warp 0 TMA, 1 the MMAs of Z and G, 18 of E, 2-17 four threads per prototype
 constexpr uint32_t E_TM_Z = 0, E_TM_G = 128, E_TM_E = 256, E_TM_DZ = 384;   // dZ: hi 64 columns, lo 64
 
 struct EBars {
-  uint64_t u_full, h_full, h_empty, x_full[E_NXS], x_empty[E_NXS], zg_full, zg_empty, dz_full, e_done, mma_done;
+  uint64_t u_full, h_full, h_empty, x_full[E_NXS], x_empty[E_NXS], zg_full, zg_empty, dz_full, e_done, mma_done[2], zg_turn, e_turn;
   uint32_t tmem_base;
   int abort;
 };
@@ -306,12 +333,16 @@ __global__ void __launch_bounds__(E_THREADS, 1)
     mbar_init(&bars->u_full, 1);
     mbar_init(&bars->h_full, 1);
     mbar_init(&bars->h_empty, 1);
-    for (int s = 0; s < E_NXS; ++s) { mbar_init(&bars->x_full[s], 1); mbar_init(&bars->x_empty[s], 1); }
+    // X is read by the MMAs of both threads
+    for (int s = 0; s < E_NXS; ++s) { mbar_init(&bars->x_full[s], 1); mbar_init(&bars->x_empty[s], 2); }
     mbar_init(&bars->zg_full, 1);
-    mbar_init(&bars->zg_empty, 256);
-    mbar_init(&bars->dz_full, 256);
+    mbar_init(&bars->zg_empty, 512);
+    mbar_init(&bars->dz_full, 512);
     mbar_init(&bars->e_done, 1);
-    mbar_init(&bars->mma_done, 1);
+    mbar_init(&bars->zg_turn, 1);
+    mbar_init(&bars->e_turn, 1);
+    mbar_init(&bars->mma_done[0], 1);
+    mbar_init(&bars->mma_done[1], 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -353,62 +384,73 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         mbar_wait_bounded(&bars->x_full[t % E_NXS], (t / E_NXS) & 1);
     }
   } else if (warp == 1 && lane == 0) {
+    // Z = (U hi + U lo) X^T, G = (dH hi + dH lo) X^T.  The turns are Z G (t + 1), then E (t): E's
+    // products run while the warps read this tile's Z and G.
     const uint32_t id_zg = idesc_bf16(128, 128, false, false);
-    const uint32_t id_e = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
     const uint64_t du = kmajor(smem_u32(smem + E_OFF_U));
-    auto x_at = [&](int t) { return smem_u32(smem + E_OFF_X + (t % E_NXS) * XT_BYTES); };
-    // E += dZ X of tile t (afresh after every drain)
-    auto emma = [&](int t) -> bool {
+    int tiles = 0;
+    if (mbar_wait(&bars->u_full, 0, abort, p.err))
+      for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int, int64_t, int64_t, bool first, bool last) {
+        if (first && !mbar_wait(&bars->h_full, piece & 1, abort, p.err)) return false;
+        if (!mbar_wait(&bars->x_full[t % E_NXS], (t / E_NXS) & 1, abort, p.err)) return false;
+        if (t > 0 && !mbar_wait(&bars->zg_empty, (t - 1) & 1, abort, p.err)) return false;
+        if (t > 1 && !mbar_wait(&bars->zg_turn, t & 1, abort, p.err)) return false;
+        tc_fence_after();
+        const uint64_t dx = kmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
+#pragma unroll
+        for (int o = 0; o < 4; ++o)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), id_zg,
+                   (o & 1) || ks > 0);
+        if (t > 0) mbar_arrive(&bars->e_turn);
+        mma_commit(&bars->zg_full);
+        mma_commit(&bars->x_empty[t % E_NXS]);
+        if (last) mma_commit(&bars->h_empty);
+        tiles = t + 1;
+        return true;
+      });
+    // the last tile's E, once the turn before it was taken (a barrier two phases on looks unfinished)
+    if (tiles < 2 || mbar_wait(&bars->zg_turn, tiles & 1, abort, p.err)) mbar_arrive(&bars->e_turn);
+    mma_commit(&bars->mma_done[0]);
+    mbar_wait_bounded(&bars->mma_done[0], 0);
+  } else if (warp == 18 && lane == 0) {
+    // E += dZ X, afresh after every drain
+    const uint32_t id_e = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
+    for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
+      // dZ was computed from Z and G of this tile, so its X is there
+      if (!mbar_wait(&bars->x_full[t % E_NXS], (t / E_NXS) & 1, abort, p.err)) return false;
       if (!mbar_wait(&bars->dz_full, t & 1, abort, p.err)) return false;
+      if (!mbar_wait(&bars->e_turn, t & 1, abort, p.err)) return false;
       tc_fence_after();
-      const uint64_t dx = mnmajor(x_at(t));
+      const uint64_t dx = mnmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
       const uint32_t kept = t % kDrain != 0 ? 1u : 0u;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, dx + mnstep(ks), id_e, ks > 0 ? 1u : kept);
         mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, dx + mnstep(ks), id_e, 1u);
       }
+      mbar_arrive(&bars->zg_turn);
       mma_commit(&bars->e_done);
       mma_commit(&bars->x_empty[t % E_NXS]);
       return true;
-    };
-    if (mbar_wait(&bars->u_full, 0, abort, p.err)) {
-      int prev = -1;
-      for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int, int64_t, int64_t, bool first, bool last) {
-        if (first && !mbar_wait(&bars->h_full, piece & 1, abort, p.err)) return false;
-        if (!mbar_wait(&bars->x_full[t % E_NXS], (t / E_NXS) & 1, abort, p.err)) return false;
-        if (t > 0 && !mbar_wait(&bars->zg_empty, (t - 1) & 1, abort, p.err)) return false;
-        tc_fence_after();
-        const uint64_t dx = kmajor(x_at(t));
-#pragma unroll
-        for (int o = 0; o < 4; ++o)                      // Z = (U hi + U lo) X^T, G = (dH hi + dH lo) X^T
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), id_zg,
-                   (o & 1) || ks > 0);
-        mma_commit(&bars->zg_full);
-        if (last) mma_commit(&bars->h_empty);
-        if (prev >= 0 && !emma(prev)) return false;
-        prev = t;
-        return true;
-      });
-      if (prev >= 0 && !*abort) emma(prev);
-    }
-    mma_commit(&bars->mma_done);
-    mbar_wait_bounded(&bars->mma_done, 0);
-  } else if (warp >= 2) {
-    const int q = warp % 4, h = (warp - 2) / 4;          // events 64 h .. 64 h + 63 of a tile, columns 64 h .. of E
-    const uint32_t lane_addr = (uint32_t)(q * 32) << 16;
+    });
+    mma_commit(&bars->mma_done[1]);
+    mbar_wait_bounded(&bars->mma_done[1], 0);
+  } else if (warp >= 2 && warp < 18) {
+    const int q = warp % 4, w = (warp - 2) / 4;          // events 32 w .. 32 w + 31 of a tile, columns 32 w .. of E
+    const uint32_t own = tmem + ((uint32_t)(q * 32) << 16) + 32 * w;
+    const uint32_t dz_at = tmem + ((uint32_t)(q * 32) << 16) + E_TM_DZ + 16 * w;
     const int j = sl * TILE + q * 32 + lane;
-    float acc[64];                                       // this thread's half row of E
+    float acc[32];                                       // this thread's quarter row of E
 #pragma unroll
-    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
     auto drain = [&]() {
 #pragma unroll
-      for (int i = 0; i < 64; i += 16) {
+      for (int i = 0; i < 32; i += 16) {
         float v[16];
-        tmem_ld16(tmem + lane_addr + E_TM_E + 64 * h + i, v);
-        tmem_wait_ld16(v);
+        tmem_ld16(own + E_TM_E + i, v);
+        wait_ld<16>(v);
 #pragma unroll
         for (int x = 0; x < 16; ++x) acc[i + x] += v[x];
       }
@@ -425,39 +467,34 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         nl2 = make_float2(-l2, -l2);
         nc = make_float2(-c, -c);
       }
+      const int nv = (int)min(pe - tb - 32 * w, (int64_t)32);   // events of this quarter that are the user's
       if (!mbar_wait(&bars->zg_full, t & 1, abort, p.err)) return ok = false;
       tc_fence_after();
-      uint32_t hi[32], lo[32];
-      const int nv = (int)min(pe - tb - 64 * h, (int64_t)64);   // events of this half that are the user's
+      float z[32], gv[32];
+      tmem_ld32(own + E_TM_Z, z);
+      tmem_ld32(own + E_TM_G, gv);
+      wait_ld<32>(z);
+      wait_ld<32>(gv);
+      tc_fence_before();
+      mbar_arrive(&bars->zg_empty);
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float z[32], gv[32];
-        tmem_ld32(tmem + lane_addr + E_TM_Z + 64 * h + 32 * c, z);
-        tmem_ld32(tmem + lane_addr + E_TM_G + 64 * h + 32 * c, gv);
-        wait_ld<32>(z);
-        wait_ld<32>(gv);
-        if (c == 1) {
-          tc_fence_before();
-          mbar_arrive(&bars->zg_empty);
+      for (int i = 0; i < 32; i += 2) {
+        const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nl2);
+        const float2 d = __fadd2_rn(make_float2(gv[i], gv[i + 1]), nc);
+        float2 dz = __fmul2_rn(make_float2(ex2(e.x), ex2(e.y)), d);
+        if (nv < 32) {
+          if (i >= nv) dz.x = 0.f;
+          if (i + 1 >= nv) dz.y = 0.f;
         }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 e = __fadd2_rn(make_float2(z[i], z[i + 1]), nl2);
-          const float2 d = __fadd2_rn(make_float2(gv[i], gv[i + 1]), nc);
-          float2 dz = __fmul2_rn(make_float2(ex2(e.x), ex2(e.y)), d);
-          if (nv < 64) {
-            if (32 * c + i >= nv) dz.x = 0.f;
-            if (32 * c + i + 1 >= nv) dz.y = 0.f;
-          }
-          split2(dz.x, dz.y, hi[16 * c + i / 2], lo[16 * c + i / 2]);
-        }
+        split2(dz.x, dz.y, hi[i / 2], lo[i / 2]);
       }
       // the last tile's E MMA has read dZ, and E is complete up to that tile
       if (t > 0 && !mbar_wait(&bars->e_done, (t - 1) & 1, abort, p.err)) return ok = false;
       tc_fence_after();
       if (t > 0 && t % kDrain == 0) drain();
-      tmem_st32(tmem + lane_addr + E_TM_DZ + 32 * h, hi);
-      tmem_st32(tmem + lane_addr + E_TM_DZ + 64 + 32 * h, lo);
+      tmem_st16(dz_at, hi);
+      tmem_st16(dz_at + 64, lo);
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars->dz_full);
@@ -468,9 +505,9 @@ __global__ void __launch_bounds__(E_THREADS, 1)
       tc_fence_after();
       drain();
       if (j < p.k) {
-        float* dst = p.Epart + ((int64_t)g * p.k + j) * DD + 64 * h;
+        float* dst = p.Epart + ((int64_t)g * p.k + j) * DD + 32 * w;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) *(float4*)(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        for (int i = 0; i < 32; i += 4) *(float4*)(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
       }
     }
   }
@@ -491,13 +528,15 @@ constexpr uint32_t X_OFF_CH = 2 * XT_BYTES;
 constexpr uint32_t X_OFF_ROW = X_OFF_CH + X_NCS * CH_BYTES;      // [X_NCS][lse2 64 | ln2 c 64]
 constexpr uint32_t X_OFF_BAR = X_OFF_ROW + X_NCS * 2 * KC * 4;
 constexpr uint32_t X_SMEM = X_OFF_BAR + 256 + 1024;
-constexpr int X_THREADS = 576;               // warp 0 TMA, 1 MMA, 2-17 four threads per token, both tiles in turn
+// warp 0 TMA, 1 and 18 the MMAs of tile 0 and tile 1, 2-17 four threads per token, both tiles in turn
+constexpr int X_THREADS = 608;
 // TMEM columns of tile i: [Z|G] at 128 i, later A and ln2 dZ as bf16 pairs in the columns of Z;
 // dX at 256 + 128 i
 constexpr uint32_t X_TM_ZG = 0, X_TM_Q = 256;
 
 struct XBars {
-  uint64_t x_full[2], x_empty[2], c_full[X_NCS], c_empty[X_NCS], zg_full[2], aa_full[2], q_full[2], mma_done;
+  uint64_t x_full[2], x_empty[2], c_full[X_NCS], c_empty[X_NCS], zg_full[2], aa_full[2], q_full[2], mma_done[2];
+  Turns turns;
   uint32_t tmem_base;
   int abort;
 };
@@ -554,9 +593,10 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       mbar_init(&bars->zg_full[i], 1);
       mbar_init(&bars->aa_full[i], 512);
       mbar_init(&bars->q_full[i], 1);
+      mbar_init(&bars->mma_done[i], 1);
+      mbar_init(&bars->turns.bar[i], 1);
     }
-    for (int s = 0; s < X_NCS; ++s) { mbar_init(&bars->c_full[s], 1); mbar_init(&bars->c_empty[s], 1); }
-    mbar_init(&bars->mma_done, 1);
+    for (int s = 0; s < X_NCS; ++s) { mbar_init(&bars->c_full[s], 1); mbar_init(&bars->c_empty[s], 2); }
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -605,70 +645,70 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       for (int c = std::max(0, cc - X_NCS); c < cc; ++c)
         mbar_wait_bounded(&bars->c_full[c % X_NCS], (c / X_NCS) & 1);
     }
-  } else if (warp == 1 && lane == 0) {
-    // ------------------------------------------------------------ MMA issuer
+  } else if (warp == 1 || warp == 18) {
+    // ------------------------------------------------------------ MMA issuers: tile i of every unit
+    const int i = warp == 18;
     const uint32_t id_zg = idesc_bf16(128, 128, false, false), id_lo = idesc_bf16(128, 64, false, false);
     const uint32_t id_q = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
-    int xt[2] = {0, 0}, at[2] = {0, 0};      // tiles begun, and stages aggregated, per tile index
-    // [Z|G] of tile i for stage counter cc: Z = X (U hi + U lo)^T, G = X dH^T
-    auto logits = [&](int i, int cc, bool first, bool last) -> bool {
-      if (first) {
-        if (!mbar_wait(&bars->x_full[i], xt[i] & 1, abort, p.err)) return false;
-        ++xt[i];
-      }
-      const int s = cc % X_NCS;
-      if (!mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) return false;
-      tc_fence_after();
-      const uint64_t dx = kmajor(smem_u32(smem + X_OFF_X + i * XT_BYTES));
-      const uint64_t dc = kmajor(smem_u32(smem + X_OFF_CH + s * CH_BYTES));
-      const uint32_t zg = tmem + X_TM_ZG + 128 * i;
+    const uint32_t zg = tmem + X_TM_ZG + 128 * i, q = tmem + X_TM_Q + 128 * i;
+    const uint64_t dx = kmajor(smem_u32(smem + X_OFF_X + i * XT_BYTES));
+    if (lane == 0) {
+      int cc = 0, x = 0, a = 0, n = 0;       // stages, tiles, aggregated stages and turns so far
+      // A turn is the aggregation of a stage and the next stage's logits.
+      // Logits for stage counter cc: Z = X (U hi + U lo)^T, G = X dH^T
+      auto logits_ready = [&](int cc, bool first) -> bool {
+        return (!first || mbar_wait(&bars->x_full[i], x++ & 1, abort, p.err)) &&
+               mbar_wait(&bars->c_full[cc % X_NCS], (cc / X_NCS) & 1, abort, p.err);
+      };
+      auto logits = [&](int cc) {
+        const uint64_t dc = kmajor(smem_u32(smem + X_OFF_CH + cc % X_NCS * CH_BYTES));
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_ss(zg, dx + kstep(ks), dc + kstep(ks), id_zg, ks > 0);
+        for (int ks = 0; ks < 8; ++ks) mma_ss(zg, dx + kstep(ks), dc + kstep(ks), id_zg, ks > 0);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks)
-        mma_ss(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_lo, 1u);
-      mma_commit(&bars->zg_full[i]);
-      if (last) mma_commit(&bars->x_empty[i]);
-      return true;
-    };
-    // dX += A dH + (ln2 dZ) U (U in base-2 units) over the stage's 64 prototypes
-    auto aggregate = [&](int i, int cc, bool first, bool last, bool frees) -> bool {
-      if (!mbar_wait(&bars->aa_full[i], at[i] & 1, abort, p.err)) return false;
-      ++at[i];
-      tc_fence_after();
-      const uint64_t dc = mnmajor(smem_u32(smem + X_OFF_CH + (cc % X_NCS) * CH_BYTES));
-      const uint32_t q = tmem + X_TM_Q + 128 * i, kept = first ? 0u : 1u;
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ss(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_lo, 1u);
+      };
+      bool ok = true;
+      for (Units un(p, g); ok && !un.done(); un.next()) {
+        const bool two = un.two();
+        if (i == 1 && !two) {
+          // no tile of this thread's: its share of freeing the unit's stages (once they were full, so
+          // that no arrival counts for an earlier use of the stage)
+          for (int c = 0; ok && c < nch; ++c, ++cc) {
+            ok = mbar_wait(&bars->c_full[cc % X_NCS], (cc / X_NCS) & 1, abort, p.err);
+            if (ok) mbar_arrive(&bars->c_empty[cc % X_NCS]);
+          }
+          continue;
+        }
+        // the first logits, then turns of aggregation and logits, then the last aggregation
+        for (int c = -1; c < nch; ++c) {
+          if (c >= 0 && !mbar_wait(&bars->aa_full[i], a++ & 1, abort, p.err)) { ok = false; break; }
+          if (c + 1 < nch && !logits_ready(cc + c + 1, c < 0)) { ok = false; break; }
+          if (two && !turn_wait(&bars->turns, i, n++, abort, p.err)) { ok = false; break; }
+          tc_fence_after();
+          if (c >= 0) {
+            // dX += A dH + (ln2 dZ) U (U in base-2 units) over the stage's 64 prototypes
+            const uint64_t dc = mnmajor(smem_u32(smem + X_OFF_CH + (cc + c) % X_NCS * CH_BYTES));
+            const uint32_t kept = c > 0 ? 1u : 0u;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        // prototypes 16 ks ..: written by the threads of quarter ks, A then dZ, 8 columns each
-        const uint32_t a = tmem + X_TM_ZG + 128 * i + 16 * ks;
-        mma_ts(q, a, dc + (8192 >> 4) + mnstep(ks), id_q, ks > 0 ? 1u : kept);
-        mma_ts(q, a + 8, dc + mnstep(ks), id_q, 1u);
+            for (int ks = 0; ks < 4; ++ks) {
+              // prototypes 16 ks ..: written by the threads of quarter ks, A then dZ, 8 columns each
+              mma_ts(q, zg + 16 * ks, dc + (8192 >> 4) + mnstep(ks), id_q, ks > 0 ? 1u : kept);
+              mma_ts(q, zg + 16 * ks + 8, dc + mnstep(ks), id_q, 1u);
+            }
+            mma_commit(&bars->c_empty[(cc + c) % X_NCS]);
+            if (c == nch - 1) mma_commit(&bars->q_full[i]);
+          }
+          if (c + 1 < nch) logits(cc + c + 1);
+          if (two) turn_pass(&bars->turns, i);
+          if (c + 1 < nch) mma_commit(&bars->zg_full[i]);
+          if (c + 1 == nch - 1) mma_commit(&bars->x_empty[i]);
+        }
+        cc += nch;
       }
-      if (frees) mma_commit(&bars->c_empty[cc % X_NCS]);
-      if (last) mma_commit(&bars->q_full[i]);
-      return true;
-    };
-    int cc = 0;
-    Units un(p, g), nx(p, g);
-    bool ok = !un.done() && logits(0, 0, true, nch == 1) && (!un.two() || logits(1, 0, true, nch == 1));
-    while (ok && !un.done()) {
-      nx.next();
-      const bool two = un.two();
-      for (int c = 0; ok && c < nch; ++c, ++cc) {
-        const bool last = c == nch - 1;
-        // what follows this stage: the unit's next prototypes, or the next unit's first
-        const bool more = !last || !nx.done(), next_two = last ? (!nx.done() && nx.two()) : two;
-        const bool nf = last, nl = last ? nch == 1 : c + 1 == nch - 1;
-        // a unit of one tile is followed by one of two only across units: tile 1's logits then
-        // have no aggregation before them
-        ok = aggregate(0, cc, c == 0, last, !two) && (!more || logits(0, cc + 1, nf, nl)) &&
-             (!two || aggregate(1, cc, c == 0, last, true)) && (!next_two || logits(1, cc + 1, nf, nl));
-      }
-      un.next();
+      mma_commit(&bars->mma_done[i]);
+      mbar_wait_bounded(&bars->mma_done[i], 0);
     }
-    mma_commit(&bars->mma_done);
-    mbar_wait_bounded(&bars->mma_done, 0);
   } else if (warp >= 2) {
     // ------------------------------------------------------------ four threads per token
     const int q = warp % 4, w = (warp - 2) / 4;          // prototypes 16 w .. 16 w + 15 of a stage

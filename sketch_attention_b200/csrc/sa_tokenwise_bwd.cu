@@ -67,10 +67,11 @@ __device__ __forceinline__ void for_each_tile(const int64_t* off, int B, const C
 // each, waiting for their own barriers during the other's turn.  Without turns they issue at the same
 // time and then wait at the same time: both stages finish late, and the tensor core idles while the
 // warps work on both (dX: 4130 clocks per two stages of 1408).
-__device__ __forceinline__ uint64_t kmajor(uint32_t addr) { return smem_desc(addr, 16, 1024, SWZ_128B); }
-__device__ constexpr uint64_t kstep(int ks) { return ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4; }
-__device__ __forceinline__ uint64_t mnmajor(uint32_t addr) { return smem_desc(addr, 16384, 1024, SWZ_128B); }
-__device__ constexpr uint64_t mnstep(int ks) { return ks * 2048 >> 4; }
+constexpr uint32_t kHi = desc_hi(1024, SWZ_128B);
+__device__ __forceinline__ uint32_t kmajor(uint32_t addr) { return desc_lo(addr, 16); }
+__device__ constexpr uint32_t kstep(int ks) { return ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4; }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t addr) { return desc_lo(addr, 16384); }
+__device__ constexpr uint32_t mnstep(int ks) { return ks * 2048 >> 4; }
 
 // x = hi + lo as bf16 pairs
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   } else if (warp == 1 || warp == 18) {
     const int b = warp == 18;                // the parity of this thread's tiles
     const uint32_t id = idesc_bf16(128, 128, false, false), z = tmem + 128 * b;
-    const uint64_t du = kmajor(smem_u32(smem + S_OFF_U)), dulo = kmajor(smem_u32(smem + S_OFF_U + XT_BYTES));
+    const uint32_t du = kmajor(smem_u32(smem + S_OFF_U)), dulo = kmajor(smem_u32(smem + S_OFF_U + XT_BYTES));
     if (lane == 0) {
       if (mbar_wait(&bars->u_full, 0, abort, p.err))
         for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t, int64_t, bool, bool) {
@@ -191,11 +192,11 @@ __global__ void __launch_bounds__(S_THREADS, 1)
           if (t >= 2 && !mbar_wait(&bars->z_empty[b], ((t >> 1) - 1) & 1, abort, p.err)) return false;
           if (!turn_wait(&bars->turns, b, t >> 1, abort, p.err)) return false;
           tc_fence_after();
-          const uint64_t dx = kmajor(smem_u32(smem + S_OFF_X + s * XT_BYTES));
+          const uint32_t dx = kmajor(smem_u32(smem + S_OFF_X + s * XT_BYTES));
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) mma_ss(z, du + kstep(ks), dx + kstep(ks), id, ks > 0);
+          for (int ks = 0; ks < 8; ++ks) mma_ss_lo(z, du + kstep(ks), dx + kstep(ks), kHi, id, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) mma_ss(z, dulo + kstep(ks), dx + kstep(ks), id, 1u);
+          for (int ks = 0; ks < 8; ++ks) mma_ss_lo(z, dulo + kstep(ks), dx + kstep(ks), kHi, id, 1u);
           turn_pass(&bars->turns, b);
           mma_commit(&bars->z_full[b]);
           mma_commit(&bars->x_empty[s]);
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(E_THREADS, 1)
     // Z = (U hi + U lo) X^T, G = (dH hi + dH lo) X^T.  The turns are Z G (t + 1), then E (t): E's
     // products run while the warps read this tile's Z and G.
     const uint32_t id_zg = idesc_bf16(128, 128, false, false);
-    const uint64_t du = kmajor(smem_u32(smem + E_OFF_U));
+    const uint32_t du = kmajor(smem_u32(smem + E_OFF_U));
     int tiles = 0;
     if (mbar_wait(&bars->u_full, 0, abort, p.err))
       for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int, int64_t, int64_t, bool first, bool last) {
@@ -396,13 +397,13 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         if (t > 0 && !mbar_wait(&bars->zg_empty, (t - 1) & 1, abort, p.err)) return false;
         if (t > 1 && !mbar_wait(&bars->zg_turn, t & 1, abort, p.err)) return false;
         tc_fence_after();
-        const uint64_t dx = kmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
+        const uint32_t dx = kmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
 #pragma unroll
         for (int o = 0; o < 4; ++o)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ss(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), id_zg,
-                   (o & 1) || ks > 0);
+            mma_ss_lo(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), kHi,
+                      id_zg, (o & 1) || ks > 0);
         if (t > 0) mbar_arrive(&bars->e_turn);
         mma_commit(&bars->zg_full);
         mma_commit(&bars->x_empty[t % E_NXS]);
@@ -423,12 +424,12 @@ __global__ void __launch_bounds__(E_THREADS, 1)
       if (!mbar_wait(&bars->dz_full, t & 1, abort, p.err)) return false;
       if (!mbar_wait(&bars->e_turn, t & 1, abort, p.err)) return false;
       tc_fence_after();
-      const uint64_t dx = mnmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
+      const uint32_t dx = mnmajor(smem_u32(smem + E_OFF_X + t % E_NXS * XT_BYTES));
       const uint32_t kept = t % kDrain != 0 ? 1u : 0u;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, dx + mnstep(ks), id_e, ks > 0 ? 1u : kept);
-        mma_ts(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, dx + mnstep(ks), id_e, 1u);
+        mma_ts_lo(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, dx + mnstep(ks), kHi, id_e, ks > 0 ? 1u : kept);
+        mma_ts_lo(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, dx + mnstep(ks), kHi, id_e, 1u);
       }
       mbar_arrive(&bars->zg_turn);
       mma_commit(&bars->e_done);
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     const uint32_t id_zg = idesc_bf16(128, 128, false, false), id_lo = idesc_bf16(128, 64, false, false);
     const uint32_t id_q = idesc_bf16(128, 128, false, true);     // A from TMEM, B MN-major
     const uint32_t zg = tmem + X_TM_ZG + 128 * i, q = tmem + X_TM_Q + 128 * i;
-    const uint64_t dx = kmajor(smem_u32(smem + X_OFF_X + i * XT_BYTES));
+    const uint32_t dx = kmajor(smem_u32(smem + X_OFF_X + i * XT_BYTES));
     if (lane == 0) {
       int cc = 0, x = 0, a = 0, n = 0;       // stages, tiles, aggregated stages and turns so far
       // A turn is the aggregation of a stage and the next stage's logits.
@@ -661,12 +662,12 @@ __global__ void __launch_bounds__(X_THREADS, 1)
                mbar_wait(&bars->c_full[cc % X_NCS], (cc / X_NCS) & 1, abort, p.err);
       };
       auto logits = [&](int cc) {
-        const uint64_t dc = kmajor(smem_u32(smem + X_OFF_CH + cc % X_NCS * CH_BYTES));
+        const uint32_t dc = kmajor(smem_u32(smem + X_OFF_CH + cc % X_NCS * CH_BYTES));
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss(zg, dx + kstep(ks), dc + kstep(ks), id_zg, ks > 0);
+        for (int ks = 0; ks < 8; ++ks) mma_ss_lo(zg, dx + kstep(ks), dc + kstep(ks), kHi, id_zg, ks > 0);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_ss(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), id_lo, 1u);
+          mma_ss_lo(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), kHi, id_lo, 1u);
       };
       bool ok = true;
       for (Units un(p, g); ok && !un.done(); un.next()) {
@@ -688,13 +689,13 @@ __global__ void __launch_bounds__(X_THREADS, 1)
           tc_fence_after();
           if (c >= 0) {
             // dX += A dH + (ln2 dZ) U (U in base-2 units) over the stage's 64 prototypes
-            const uint64_t dc = mnmajor(smem_u32(smem + X_OFF_CH + (cc + c) % X_NCS * CH_BYTES));
+            const uint32_t dc = mnmajor(smem_u32(smem + X_OFF_CH + (cc + c) % X_NCS * CH_BYTES));
             const uint32_t kept = c > 0 ? 1u : 0u;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
               // prototypes 16 ks ..: written by the threads of quarter ks, A then dZ, 8 columns each
-              mma_ts(q, zg + 16 * ks, dc + (8192 >> 4) + mnstep(ks), id_q, ks > 0 ? 1u : kept);
-              mma_ts(q, zg + 16 * ks + 8, dc + mnstep(ks), id_q, 1u);
+              mma_ts_lo(q, zg + 16 * ks, dc + (8192 >> 4) + mnstep(ks), kHi, id_q, ks > 0 ? 1u : kept);
+              mma_ts_lo(q, zg + 16 * ks + 8, dc + mnstep(ks), kHi, id_q, 1u);
             }
             mma_commit(&bars->c_empty[(cc + c) % X_NCS]);
             if (c == nch - 1) mma_commit(&bars->q_full[i]);

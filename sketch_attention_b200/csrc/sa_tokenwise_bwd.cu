@@ -86,8 +86,16 @@ __device__ __forceinline__ void wait_ld(float* v) {
   for (int i = 0; i < N; i += 16) tmem_wait_ld16(v + i);
 }
 
+// mbar_wait of a whole warp, with one answer: the lanes leave together when the kernel gives up, so
+// that no warp-wide instruction (tcgen05.ld) waits for lanes that have left.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+
 // The turns of the two issuing threads: thread 0 goes first, then they alternate (n: turns taken so
-// far).  A turn ends when its products are issued, not when they are complete.
+// far).  A turn is passed on kEarly products before its last is issued: the other thread's wake-up takes
+// about as long as those run.
+constexpr int kEarly = 4;
 struct Turns {
   uint64_t bar[2];
 };
@@ -196,8 +204,10 @@ __global__ void __launch_bounds__(S_THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) mma_ss_lo(z, du + kstep(ks), dx + kstep(ks), kHi, id, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) mma_ss_lo(z, dulo + kstep(ks), dx + kstep(ks), kHi, id, 1u);
-          turn_pass(&bars->turns, b);
+          for (int ks = 0; ks < 8; ++ks) {
+            if (ks == 8 - kEarly) turn_pass(&bars->turns, b);
+            mma_ss_lo(z, dulo + kstep(ks), dx + kstep(ks), kHi, id, 1u);
+          }
           mma_commit(&bars->z_full[b]);
           mma_commit(&bars->x_empty[s]);
           return true;
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
       if (first) { m = -INFINITY; sum = 0.f; }
       const int nv = (int)min(pe - tb - 64 * h, (int64_t)64);   // events of this half that are the user's
       if ((t & 1) == team) {
-        if (!mbar_wait(&bars->z_full[team], (t >> 1) & 1, abort, p.err)) return false;
+        if (!warp_wait(&bars->z_full[team], (t >> 1) & 1, abort, p.err)) return false;
         tc_fence_after();
         float z[64];
         tmem_ld32(at, z);
@@ -401,10 +411,11 @@ __global__ void __launch_bounds__(E_THREADS, 1)
 #pragma unroll
         for (int o = 0; o < 4; ++o)
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
+          for (int ks = 0; ks < 8; ++ks) {
+            if (o == 3 && ks == 8 - kEarly && t > 0) mbar_arrive(&bars->e_turn);
             mma_ss_lo(tmem + (o < 2 ? E_TM_Z : E_TM_G), du + (o * XT_BYTES >> 4) + kstep(ks), dx + kstep(ks), kHi,
                       id_zg, (o & 1) || ks > 0);
-        if (t > 0) mbar_arrive(&bars->e_turn);
+          }
         mma_commit(&bars->zg_full);
         mma_commit(&bars->x_empty[t % E_NXS]);
         if (last) mma_commit(&bars->h_empty);
@@ -428,10 +439,10 @@ __global__ void __launch_bounds__(E_THREADS, 1)
       const uint32_t kept = t % kDrain != 0 ? 1u : 0u;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
+        if (ks == 8 - kEarly / 2) mbar_arrive(&bars->zg_turn);
         mma_ts_lo(tmem + E_TM_E, tmem + E_TM_DZ + ks * 8, dx + mnstep(ks), kHi, id_e, ks > 0 ? 1u : kept);
         mma_ts_lo(tmem + E_TM_E, tmem + E_TM_DZ + 64 + ks * 8, dx + mnstep(ks), kHi, id_e, 1u);
       }
-      mbar_arrive(&bars->zg_turn);
       mma_commit(&bars->e_done);
       mma_commit(&bars->x_empty[t % E_NXS]);
       return true;
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         nc = make_float2(-c, -c);
       }
       const int nv = (int)min(pe - tb - 32 * w, (int64_t)32);   // events of this quarter that are the user's
-      if (!mbar_wait(&bars->zg_full, t & 1, abort, p.err)) return ok = false;
+      if (!warp_wait(&bars->zg_full, t & 1, abort, p.err)) return ok = false;
       tc_fence_after();
       float z[32], gv[32];
       tmem_ld32(own + E_TM_Z, z);
@@ -491,7 +502,7 @@ __global__ void __launch_bounds__(E_THREADS, 1)
         split2(dz.x, dz.y, hi[i / 2], lo[i / 2]);
       }
       // the last tile's E MMA has read dZ, and E is complete up to that tile
-      if (t > 0 && !mbar_wait(&bars->e_done, (t - 1) & 1, abort, p.err)) return ok = false;
+      if (t > 0 && !warp_wait(&bars->e_done, (t - 1) & 1, abort, p.err)) return ok = false;
       tc_fence_after();
       if (t > 0 && t % kDrain == 0) drain();
       tmem_st16(dz_at, hi);
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(E_THREADS, 1)
       tiles = t + 1;
       return true;
     });
-    if (ok && tiles > 0 && mbar_wait(&bars->e_done, (tiles - 1) & 1, abort, p.err)) {
+    if (ok && tiles > 0 && warp_wait(&bars->e_done, (tiles - 1) & 1, abort, p.err)) {
       tc_fence_after();
       drain();
       if (j < p.k) {
@@ -661,13 +672,15 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         return (!first || mbar_wait(&bars->x_full[i], x++ & 1, abort, p.err)) &&
                mbar_wait(&bars->c_full[cc % X_NCS], (cc / X_NCS) & 1, abort, p.err);
       };
-      auto logits = [&](int cc) {
+      auto logits = [&](int cc, bool two) {
         const uint32_t dc = kmajor(smem_u32(smem + X_OFF_CH + cc % X_NCS * CH_BYTES));
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_ss_lo(zg, dx + kstep(ks), dc + kstep(ks), kHi, id_zg, ks > 0);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ++ks) {
+          if (ks == 8 - kEarly && two) turn_pass(&bars->turns, i);
           mma_ss_lo(zg, dx + kstep(ks), dc + ((32768 + (ks >> 2) * 8192 + (ks & 3) * 32) >> 4), kHi, id_lo, 1u);
+        }
       };
       bool ok = true;
       for (Units un(p, g); ok && !un.done(); un.next()) {
@@ -700,8 +713,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
             mma_commit(&bars->c_empty[(cc + c) % X_NCS]);
             if (c == nch - 1) mma_commit(&bars->q_full[i]);
           }
-          if (c + 1 < nch) logits(cc + c + 1);
-          if (two) turn_pass(&bars->turns, i);
+          if (c + 1 < nch) logits(cc + c + 1, two);
+          else if (two) turn_pass(&bars->turns, i);
           if (c + 1 < nch) mma_commit(&bars->zg_full[i]);
           if (c + 1 == nch - 1) mma_commit(&bars->x_empty[i]);
         }
@@ -728,8 +741,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
           if (i >= n_tiles) break;
           const uint32_t own = lane_addr + X_TM_ZG + 128 * i + 16 * w;
-          if (!mbar_wait(&bars->zg_full[i], a[i] & 1, abort, p.err) ||
-              !mbar_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) { ok = false; break; }
+          if (!warp_wait(&bars->zg_full[i], a[i] & 1, abort, p.err) ||
+              !warp_wait(&bars->c_full[s], (cc / X_NCS) & 1, abort, p.err)) { ok = false; break; }
           ++a[i];
           tc_fence_after();
           float z[16], gv[16];
@@ -761,7 +774,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
       }
       // this thread's 32 columns of its token's dX, in both tiles
       for (int i = 0; ok && i < n_tiles; ++i) {
-        if (!mbar_wait(&bars->q_full[i], t[i] & 1, abort, p.err)) { ok = false; break; }
+        if (!warp_wait(&bars->q_full[i], t[i] & 1, abort, p.err)) { ok = false; break; }
         ++t[i];
         tc_fence_after();
         const int64_t r = un.tb + i * TILE + row;

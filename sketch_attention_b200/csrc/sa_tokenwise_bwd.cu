@@ -273,34 +273,39 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   }
 }
 
-// lse2[u, j] = log2 of the row's sum of 2^z over the user's events, from the pieces in chunk
-// order; +inf for a padding prototype (its A = 2^(z - inf) = 0) and for a user without events
-__global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __restrict__ off, int B, Chunking ch, int k,
-                                                             int kp, const float2* __restrict__ user,
+// lse2[u, j] = log2 of the row's sum of 2^z over the user's events, from its pieces' parts; +inf for
+// a padding prototype (its A = 2^(z - inf) = 0) and for a user without events.  A CTA takes 32
+// prototypes of a user; its 8 warps take the pieces in turn, and their results are added in order.
+__global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __restrict__ off, Chunking ch, int k, int kp,
+                                                             const float2* __restrict__ user,
                                                              const float2* __restrict__ slot, float* __restrict__ lse2) {
-  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < (int64_t)B * kp; r += (int64_t)gridDim.x * 256) {
-    const int u = (int)(r / kp), j = (int)(r % kp);
-    const int64_t ub = off[u], ue = off[u + 1];
-    float lse = INFINITY;
-    if (j < k && ue > ub) {
-      const int64_t gf = ub / ch.T, gl = (ue - 1) / ch.T;
-      float m = -INFINITY, s = 0.f;
-      for (int64_t g = gf; g <= gl; ++g) {
-        const float2* p = gf == gl ? user + (int64_t)u * S_PARTS * kp
-                                   : slot + (g * 2 + (g == gf ? 1 : 0)) * S_PARTS * kp;
+  __shared__ float2 part[8][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int u = blockIdx.x / (kp / 32), j = blockIdx.x % (kp / 32) * 32 + lane;
+  const int64_t ub = off[u], ue = off[u + 1];
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](const float2& v) {
+    if (v.x == -INFINITY && v.y == 0.f) return;          // a part without events
+    const float mn = fmaxf(m, v.x);
+    s = s * exp2f(m - mn) + v.y * exp2f(v.x - mn);
+    m = mn;
+  };
+  if (ue > ub) {
+    const int64_t gf = ub / ch.T, gl = (ue - 1) / ch.T;
+    for (int64_t g = gf + warp; g <= gl; g += 8) {
+      const float2* p = gf == gl ? user + (int64_t)u * S_PARTS * kp : slot + (g * 2 + (g == gf ? 1 : 0)) * S_PARTS * kp;
+      float2 v[S_PARTS];
 #pragma unroll
-        for (int h = 0; h < S_PARTS; ++h) {
-          const float2 v = p[(int64_t)h * kp + j];
-          if (v.x == -INFINITY && v.y == 0.f) continue;  // a part without events
-          const float mn = fmaxf(m, v.x);
-          s = s * exp2f(m - mn) + v.y * exp2f(v.x - mn);
-          m = mn;
-        }
-      }
-      lse = m + log2f(s);
+      for (int h = 0; h < S_PARTS; ++h) v[h] = p[(int64_t)h * kp + j];
+#pragma unroll
+      for (int h = 0; h < S_PARTS; ++h) add(v[h]);
     }
-    lse2[r] = lse;
   }
+  part[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp > 0) return;
+  for (int w = 1; w < 8; ++w) add(part[w][lane]);
+  lse2[(int64_t)u * kp + j] = j < k && ue > ub ? m + log2f(s) : INFINITY;
 }
 
 // ============================================================== E kernel
@@ -802,77 +807,71 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 }
 
 // ============================================================== rows of 128 columns
-// The products with the d x d weights, in fp32 FMA, R rows per CTA step (the framework's tiled fp32
+// The products with the d x d weights, in fp32 FMA, 16 rows per CTA step (the framework's tiled fp32
 // GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
 // carry E back to the weights took two thirds of a small call).  A weight matrix lies in shared
-// memory (read once per CTA), [term][column] with a pitch of 132; a thread has four columns of R / 8
-// rows, a warp all columns, so its reads of a row are broadcasts and a row's sums are a shuffle.
-constexpr int R_THREADS = 256, W_PITCH = DD + 4;
-constexpr uint32_t W_BYTES = DD * W_PITCH * 4;
-constexpr int RP = 32, RW = 16;              // rows per step of the prepare and the weights kernel
-constexpr uint32_t PREP_SMEM = 2 * W_BYTES + 2 * RP * DD * 4, WEIGHTS_SMEM = 2 * W_BYTES + 3 * RW * DD * 4;
+// memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
+// without bank conflicts, so it serves W and W^T.  A thread has one column and every other four of the
+// 128 terms, 16 sums in registers; the half-warps' halves are added by a shuffle.
+constexpr int RB = 16, R_THREADS = 256, W_PITCH = DD + 4;
+constexpr uint32_t W_BYTES = DD * W_PITCH * 4, ROWS_BYTES = RB * DD * 4;
+constexpr uint32_t PREP_SMEM = W_BYTES + 3 * ROWS_BYTES, WEIGHTS_SMEM = 2 * W_BYTES + 3 * ROWS_BYTES;
 
-// w[e][c] = W[e][c]
-__device__ __forceinline__ void load_weight(float* w, const float* __restrict__ W) {
-#pragma unroll 8
-  for (int i = threadIdx.x; i < DD * DD / 4; i += R_THREADS)
-    *(float4*)(w + i / 32 * W_PITCH + i % 32 * 4) = __ldg((const float4*)W + i);
+__device__ __forceinline__ void copy16(float* dst, const float* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// w[e][c] = W[c][e]: a warp stores one term of 32 columns at a time
-__device__ __forceinline__ void load_weight_transposed(float* w, const float* __restrict__ W) {
-#pragma unroll 8
-  for (int i = threadIdx.x; i < DD * DD / 4; i += R_THREADS) {
-    const int c = i % DD, e = i / DD * 4;
-    const float4 x = __ldg((const float4*)(W + c * DD + e));
-    w[e * W_PITCH + c] = x.x;
-    w[(e + 1) * W_PITCH + c] = x.y;
-    w[(e + 2) * W_PITCH + c] = x.z;
-    w[(e + 3) * W_PITCH + c] = x.w;
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// the copies of a weight matrix, and of `have` rows (the others zeros); copies_done, then a barrier
+__device__ __forceinline__ void load_weight(float* w, const float* __restrict__ W) {
+#pragma unroll
+  for (int x = 0; x < DD * DD / 4 / R_THREADS; ++x) {
+    const int i = x * R_THREADS + threadIdx.x;
+    copy16(w + i / 32 * W_PITCH + i % 32 * 4, W + i * 4);
   }
 }
-// rows[r] = src[r] (d floats each) for r < have, else zeros
-template <int R>
 __device__ __forceinline__ void load_block(float (*rows)[DD], const float* __restrict__ src, int have) {
 #pragma unroll
-  for (int i = threadIdx.x; i < R * DD / 4; i += R_THREADS)
-    ((float4*)rows)[i] = i / (DD / 4) < have ? __ldg((const float4*)src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x = 0; x < RB * DD / 4 / R_THREADS; ++x) {
+    const int i = x * R_THREADS + threadIdx.x;
+    if (i / 32 < have) copy16(&rows[0][0] + i * 4, src + i * 4);
+    else ((float4*)rows)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 }
 
-// out[x][.] = sum_e rows[R / 8 warp + x][e] w[e][4 lane ..]
-template <int R>
-__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float (*out)[4]) {
-  constexpr int N = R / 8;
-  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N;
+// out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e], col = 16 warp + lane % 16; in both half-warps
+template <bool kT>
+__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float* out) {
+  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 4;
 #pragma unroll
-  for (int x = 0; x < N; ++x)
+  for (int r = 0; r < RB; ++r) out[r] = 0.f;
+#pragma unroll 2
+  for (int e = e0; e < DD; e += 8) {
+    float4 v;
+    if (kT) v = *(const float4*)(w + col * W_PITCH + e);
+    else v = make_float4(w[e * W_PITCH + col], w[(e + 1) * W_PITCH + col], w[(e + 2) * W_PITCH + col],
+                         w[(e + 3) * W_PITCH + col]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[x][i] = 0.f;
-#pragma unroll 4
-  for (int e = 0; e < DD; e += 4) {
-    float4 v[4];
-#pragma unroll
-    for (int y = 0; y < 4; ++y) v[y] = *(const float4*)(w + (e + y) * W_PITCH + lane * 4);
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const float4 r4 = *(const float4*)&rows[r0 + x][e];
-      const float rv[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        out[x][0] = fmaf(rv[y], v[y].x, out[x][0]);
-        out[x][1] = fmaf(rv[y], v[y].y, out[x][1]);
-        out[x][2] = fmaf(rv[y], v[y].z, out[x][2]);
-        out[x][3] = fmaf(rv[y], v[y].w, out[x][3]);
-      }
+    for (int r = 0; r < RB; ++r) {
+      const float4 x = *(const float4*)&rows[r][e];
+      out[r] = fmaf(x.x, v.x, fmaf(x.y, v.y, fmaf(x.z, v.z, fmaf(x.w, v.w, out[r]))));
     }
   }
+#pragma unroll
+  for (int r = 0; r < RB; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
+}
+// f times the product's column into rows (each half-warp stores half of them)
+__device__ __forceinline__ void store_column(float (*rows)[DD], const float* v, float f) {
+  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, h = threadIdx.x % 32 / 16;
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+    if (r / (RB / 2) == h) rows[r][col] = f * v[r];
 }
 
 // acc[8][8] += sum_r a[r][8 ty ..] b[r][4 tx .. and 64 + 4 tx ..]: a thread's tile of a^T b
-template <int R>
 __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)[DD], float (*acc)[8]) {
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll 2
-  for (int r = 0; r < R; ++r) {
+  for (int r = 0; r < RB; ++r) {
     const float4 a0 = *(const float4*)&a[r][8 * ty], a1 = *(const float4*)&a[r][8 * ty + 4];
     const float4 b0 = *(const float4*)&b[r][4 * tx], b1 = *(const float4*)&b[r][64 + 4 * tx];
     const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
@@ -893,78 +892,74 @@ __device__ __forceinline__ void store_outer(float* __restrict__ part, const floa
   }
 }
 // four columns of a row as hi + lo bf16
-__device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo, int64_t at, const float* x) {
+__device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo, int64_t at, const float4& x) {
   uint2 h, l;
-  split2(x[0], x[1], h.x, l.x);
-  split2(x[2], x[3], h.y, l.y);
+  split2(x.x, x.y, h.x, l.x);
+  split2(x.z, x.w, h.y, l.y);
   *(uint2*)(hi + at) = h;
   *(uint2*)(lo + at) = l;
 }
 
-// CTAs [0, kp / 32): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others, 32 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
+// CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
+// The others, 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
 // (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
-__global__ void __launch_bounds__(R_THREADS, 1) tw_prepare_kernel(
+__global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
     const float* __restrict__ W_Q, const float* __restrict__ W_K, const float* __restrict__ W_V,
     const float* __restrict__ dS, const float* __restrict__ H, float* __restrict__ Q, __nv_bfloat16* __restrict__ Uhi,
     __nv_bfloat16* __restrict__ Ulo, __nv_bfloat16* __restrict__ Hhi, __nv_bfloat16* __restrict__ Hlo,
     float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v) {
   extern __shared__ __align__(16) float sm[];
-  float *w0 = sm, *w1 = sm + DD * W_PITCH;
-  float (*a)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*b)[DD] = a + RP;
-  constexpr int N = RP / 8;
-  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N, groups = kp / RP;
-  float v[N][4];
+  float (*a)[DD] = (float (*)[DD])(sm + DD * W_PITCH), (*b)[DD] = a + RB, (*o)[DD] = b + RB;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / RB;
+  float v[RB];
   if ((int)blockIdx.x < groups) {
-    const int j0 = blockIdx.x * RP;
-    load_block<RP>(a, P + (int64_t)j0 * DD, k - j0);
-    load_weight(w0, W_Q);
-    load_weight_transposed(w1, W_K);
+    const int j0 = blockIdx.x * RB;
+    load_block(a, P + (int64_t)j0 * DD, k - j0);
+    load_weight(sm, W_Q);
+    copies_done();
     __syncthreads();
-    rows_product<RP>(a, w0, v);
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const float4 q = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
-      *(float4*)&b[r0 + x][lane * 4] = q;    // read back by this warp only
-      if (j0 + r0 + x < k) *(float4*)(Q + (int64_t)(j0 + r0 + x) * DD + lane * 4) = q;
-    }
-    __syncwarp();
-    rows_product<RP>(b, w1, v);
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[x][i] *= u_scale;
-      store_split(Uhi, Ulo, (int64_t)(j0 + r0 + x) * DD + lane * 4, v[x]);
-    }
+    rows_product<false>(a, sm, v);
+    store_column(b, v, 1.f);
+    __syncthreads();
+    load_weight(sm, W_K);
+    for (int r = warp; r < RB; r += R_THREADS / 32)
+      if (j0 + r < k) *(float4*)(Q + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&b[r][lane * 4];
+    copies_done();
+    __syncthreads();
+    rows_product<true>(b, sm, v);
+    store_column(o, v, u_scale);
+    __syncthreads();
+    for (int r = warp; r < RB; r += R_THREADS / 32)
+      store_split(Uhi, Ulo, (int64_t)(j0 + r) * DD + lane * 4, *(const float4*)&o[r][lane * 4]);
     return;
   }
   const int part = blockIdx.x - groups, parts = gridDim.x - groups;
   float dwv[8][8] = {};
-  load_weight_transposed(w0, W_V);
+  load_weight(sm, W_V);
   for (int64_t g = part; g < (int64_t)B * groups; g += parts) {
-    const int u = (int)(g / groups), j0 = (int)(g % groups) * RP;
+    const int u = (int)(g / groups), j0 = (int)(g % groups) * RB;
     const int have = off[u + 1] > off[u] ? k - j0 : 0;
-    const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0 + r0;
+    const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0;
     __syncthreads();
-    load_block<RP>(a, dS + in, have);
-    load_block<RP>(b, H + in, have);
+    load_block(a, dS + in, have);
+    load_block(b, H + in, have);
+    copies_done();
     __syncthreads();
-    rows_product<RP>(a, w0, v);
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const float4 hv = *(const float4*)&b[r0 + x][lane * 4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[x][i] *= inv;
-      float dot = fmaf(v[x][0], hv.x, fmaf(v[x][1], hv.y, fmaf(v[x][2], hv.z, v[x][3] * hv.w)));
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    rows_product<true>(a, sm, v);
+    store_column(o, v, inv);
+    add_outer(b, a, dwv);
+    __syncthreads();
+    for (int r = warp; r < RB; r += R_THREADS / 32) {
+      const float4 x = *(const float4*)&o[r][lane * 4], hv = *(const float4*)&b[r][lane * 4];
+      float dot = fmaf(x.x, hv.x, fmaf(x.y, hv.y, fmaf(x.z, hv.z, x.w * hv.w)));
+      for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
       if (lane == 0) {
-        cj[row0 + x] = dot;
-        c2[row0 + x] = kLn2 * dot;
+        cj[row0 + r] = dot;
+        c2[row0 + r] = kLn2 * dot;
       }
-      store_split(Hhi, Hlo, (row0 + x) * DD + lane * 4, v[x]);
+      store_split(Hhi, Hlo, (row0 + r) * DD + lane * 4, x);
     }
-    add_outer<RP>(b, a, dwv);
   }
   store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
 }
@@ -979,43 +974,40 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
                                                                   float* __restrict__ part_qk) {
   extern __shared__ __align__(16) float sm[];
   float *w0 = sm, *w1 = sm + DD * W_PITCH;
-  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW;
-  constexpr int N = RW / 8;
-  const int lane = threadIdx.x % 32, r0 = threadIdx.x / 32 * N;
-  float dwq[8][8] = {}, dwk[8][8] = {}, v[N][4];
+  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RB, (*dq)[DD] = q + RB;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  float dwq[8][8] = {}, dwk[8][8] = {}, v[RB];
   load_weight(w0, W_K);
-  load_weight_transposed(w1, W_Q);
-  for (int j0 = blockIdx.x * RW; j0 < k; j0 += gridDim.x * RW) {
+  load_weight(w1, W_Q);
+  for (int j0 = blockIdx.x * RB; j0 < k; j0 += gridDim.x * RB) {
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < N; ++x) {
+    load_block(q, Q + (int64_t)j0 * DD, k - j0);
+    for (int r = warp; r < RB; r += R_THREADS / 32) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j0 + r0 + x < k) {
-        const float* src = Epart + (int64_t)(j0 + r0 + x) * DD + lane * 4;
+      if (j0 + r < k) {
+        const float* src = Epart + (int64_t)(j0 + r) * DD + lane * 4;
 #pragma unroll 8
         for (int g = 0; g < G; ++g) {
           const float4 y = *(const float4*)(src + (int64_t)g * k * DD);
           s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
         }
       }
-      *(float4*)&e[r0 + x][lane * 4] = s;
+      *(float4*)&e[r][lane * 4] = s;
     }
-    load_block<RW>(q, Q + (int64_t)j0 * DD, k - j0);
+    copies_done();
     __syncthreads();
-    add_outer<RW>(e, q, dwk);
-    rows_product<RW>(e, w0, v);
-#pragma unroll
-    for (int x = 0; x < N; ++x)
-      *(float4*)&dq[r0 + x][lane * 4] = make_float4(v[x][0] * rs, v[x][1] * rs, v[x][2] * rs, v[x][3] * rs);
-    __syncthreads();                         // q is no longer read: the rows of P replace it
-    load_block<RW>(q, P + (int64_t)j0 * DD, k - j0);
-    rows_product<RW>(dq, w1, v);
-#pragma unroll
-    for (int x = 0; x < N; ++x)
-      if (j0 + r0 + x < k)
-        *(float4*)(dP + (int64_t)(j0 + r0 + x) * DD + lane * 4) = make_float4(v[x][0], v[x][1], v[x][2], v[x][3]);
+    rows_product<false>(e, w0, v);
+    store_column(dq, v, rs);
+    add_outer(e, q, dwk);
+    __syncthreads();                         // q and e are no longer read: P and dP replace them
+    load_block(q, P + (int64_t)j0 * DD, k - j0);
+    rows_product<true>(dq, w1, v);
+    store_column(e, v, 1.f);
+    copies_done();
     __syncthreads();
-    add_outer<RW>(q, dq, dwq);
+    for (int r = warp; r < RB; r += R_THREADS / 32)
+      if (j0 + r < k) *(float4*)(dP + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&e[r][lane * 4];
+    add_outer(q, dq, dwq);
   }
   store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq, 1.f);
   store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk, rs);
@@ -1058,11 +1050,8 @@ Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
 // CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again)
-int value_parts(int B, int k) {
-  const int groups = padded_k(k) / RP;
-  return (int)std::min<int64_t>((int64_t)B * groups, std::max(32, device_info().sm_count - groups));
-}
-int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
+int value_parts(int B, int k) { return (int)std::min<int64_t>((int64_t)B * (padded_k(k) / RB), 128); }
+int weight_parts(int k) { return std::min((k + RB - 1) / RB, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
 
 sa_status map_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_rows) {
@@ -1103,7 +1092,7 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
   const float rs = 1.f / sqrtf((float)a.d);
   sa_status s;
   SA_TIMED("tw_prepare_kernel", st,
-           (tw_prepare_kernel<<<kp / RP + n_v, R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
+           (tw_prepare_kernel<<<kp / RB + n_v, R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
                                                                    a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi, w.Ulo,
                                                                    w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
   if (a.n_total > 0) {
@@ -1121,8 +1110,8 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
     SA_TIMED("tw_lse_kernel", st,
              (tw_lse_kernel<<<w.chE.G * slices, S_THREADS, S_SMEM, st>>>(tmX, tmU, tmUlo, sp)));
     SA_TIMED("tw_lse_combine_kernel", st,
-             (tw_lse_combine_kernel<<<(unsigned)std::min<int64_t>((hrows + 255) / 256, 4096), 256, 0, st>>>(
-                 a.off_dev, a.B, w.chE, a.k, kp, w.stat_user, w.stat_slot, w.lse2)));
+             (tw_lse_combine_kernel<<<(unsigned)(hrows / 32), 256, 0, st>>>(a.off_dev, w.chE, a.k, kp, w.stat_user,
+                                                                            w.stat_slot, w.lse2)));
     XParams xp{a.off_dev, a.B, w.chX, kp, w.lse2, w.c2, (__nv_bfloat16*)a.dX, device_status_word()};
     SA_TIMED("tw_dx_kernel", st, (tw_dx_kernel<<<w.chX.G, X_THREADS, X_SMEM, st>>>(tmX, tmU64, tmUlo64, tmH64, xp)));
     EParams ep{a.off_dev, a.B, w.chE, slices, a.k, kp, w.lse2, w.c, w.Epart, device_status_word()};

@@ -46,6 +46,28 @@ void prof_end(const char* name, cudaStream_t st);
     ::sa::prof_end(name, st);                                          \
   } while (0)
 
+// Programmatic dependent launch: a kernel launched by launch_after may start while the kernel before
+// it in the stream still runs (once all of that kernel's CTAs have called let_next_start or ended).
+// It calls wait_for_previous, which returns when the kernel before it has completed and its writes are
+// visible, before it touches anything that an earlier kernel of the call writes; setup and reads of the
+// caller's inputs may come first.  In an ordinary launch both calls do nothing.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... Params, class... Args>
+void launch_after(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);   // the caller's launch check reads the error
+}
+
 // Device error word (defined in api.cu): kernels whose bounded waits expire
 // OR in a code; sa_poll_device_status reads and clears it.
 // bits of the device status word: a bounded wait expired; an embedding id was out of

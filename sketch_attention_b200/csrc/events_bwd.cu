@@ -255,6 +255,7 @@ __device__ void sort_pass(const In& in, const SortArgs& s, int q, int shift, int
 
 __global__ void __launch_bounds__(kSortThreads + 32, 1) sort_events_kernel(SortArgs s) {
   extern __shared__ __align__(128) char smem_raw[];
+  let_next_start();
   if (threadIdx.x >= kSortThreads) {
     const int lane = threadIdx.x % 32;
     for (int i = lane; i < kZeroBytes / 16; i += 32) ((float4*)smem_raw)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -330,6 +331,8 @@ __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
     int n_actions, int d, float* __restrict__ first, float* __restrict__ last, uint32_t* __restrict__ first_key,
     uint32_t* __restrict__ open_key, float* __restrict__ d_item, float* __restrict__ action_part) {
   extern __shared__ float4 tables[];                 // [kSumWarps][n_actions][32]
+  let_next_start();
+  wait_for_previous();
   constexpr int kBatch = batch_rows<T>();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float4* mine = tables + warp * n_actions * 32 + lane;
@@ -445,6 +448,7 @@ __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32
                                                                     float* __restrict__ d_action) {
   __shared__ Cols part[kSumWarps][32];
   __shared__ int64_t long_end[kSumWarps];
+  wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if ((int)blockIdx.x < action_ctas) {
     const int a = (int)blockIdx.x;
@@ -509,6 +513,7 @@ __global__ void action_rows_kernel(const T* __restrict__ dX, const int32_t* __re
                                    const uint8_t* __restrict__ acts, int64_t n, int64_t per, int64_t vocab,
                                    int n_actions, int d, float* __restrict__ part, int* err) {
   extern __shared__ float4 tables[];                 // [warps][n_actions][32]
+  let_next_start();
   constexpr int kBatch = batch_rows<T>();
   const int warp = threadIdx.x / 32, warps = blockDim.x / 32, lane = threadIdx.x % 32;
   const int c = blockIdx.y * 128 + lane * 4;
@@ -605,19 +610,18 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
       const int smem = kSumWarps * n_actions * 512;
       set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done[2], mu);
       SA_TIMED("window_rows_kernel", st,
-               (window_rows_kernel<T, true><<<window_ctas, kSumThreads, smem, st>>>(
-                   dX, list, acts, n, win, vocab, n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item,
-                   w.action_part)));
+               launch_after(window_rows_kernel<T, true>, window_ctas, kSumThreads, smem, st, dX, list, acts, n, win, vocab,
+                            n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item, w.action_part));
     } else {
       SA_TIMED("window_rows_kernel", st,
-               (window_rows_kernel<T, false><<<window_ctas, kSumThreads, 0, st>>>(
-                   dX, list, acts, n, win, vocab, 0, d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr)));
+               launch_after(window_rows_kernel<T, false>, window_ctas, kSumThreads, 0, st, dX, list, acts, n, win, vocab, 0,
+                            d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr));
     }
   }
   const int ac = d_action ? n_actions : 0;
   SA_TIMED("crossing_rows_kernel", st,
-           (crossing_rows_kernel<<<ac + (d_item ? window_ctas : 0), kSumThreads, 0, st>>>(
-               w.first_key, w.open_key, windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action)));
+           launch_after(crossing_rows_kernel, ac + (d_item ? window_ctas : 0), kSumThreads, 0, st, w.first_key, w.open_key,
+                        windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action));
   return SA_OK;
 }
 }  // namespace

@@ -167,6 +167,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  let_next_start();
+  wait_for_previous();
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
@@ -280,6 +282,8 @@ __global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __re
                                                              const float2* __restrict__ user,
                                                              const float2* __restrict__ slot, float* __restrict__ lse2) {
   __shared__ float2 part[8][32];
+  let_next_start();
+  wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int u = blockIdx.x / (kp / 32), j = blockIdx.x % (kp / 32) * 32 + lane;
   const int64_t ub = off[u], ue = off[u + 1];
@@ -370,6 +374,8 @@ __global__ void __launch_bounds__(E_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  let_next_start();
+  wait_for_previous();
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
@@ -625,6 +631,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  let_next_start();
+  wait_for_previous();
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -807,15 +815,16 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 }
 
 // ============================================================== rows of 128 columns
-// The products with the d x d weights, in fp32 FMA, 16 rows per CTA step (the framework's tiled fp32
+// The products with the d x d weights, in fp32 FMA, 16 or 8 rows per CTA step (the framework's tiled fp32
 // GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
 // carry E back to the weights took two thirds of a small call).  A weight matrix lies in shared
 // memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
 // without bank conflicts, so it serves W and W^T.  A thread has one column and every other four of the
-// 128 terms, 16 sums in registers; the half-warps' halves are added by a shuffle.
-constexpr int RB = 16, R_THREADS = 256, W_PITCH = DD + 4;
-constexpr uint32_t W_BYTES = DD * W_PITCH * 4, ROWS_BYTES = RB * DD * 4;
-constexpr uint32_t PREP_SMEM = W_BYTES + 3 * ROWS_BYTES, WEIGHTS_SMEM = 2 * W_BYTES + 3 * ROWS_BYTES;
+// 128 terms, a sum per row in registers; the half-warps' halves are added by a shuffle.
+constexpr int R_THREADS = 256, W_PITCH = DD + 4;
+constexpr int RB = 16, RW = 8;                // rows per step of the prepare and the weights kernel
+constexpr uint32_t W_BYTES = DD * W_PITCH * 4, ROW_BYTES = DD * 4;
+constexpr uint32_t PREP_SMEM = W_BYTES + 3 * RB * ROW_BYTES, WEIGHTS_SMEM = 2 * W_BYTES + 3 * RW * ROW_BYTES;
 
 __device__ __forceinline__ void copy16(float* dst, const float* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -829,9 +838,10 @@ __device__ __forceinline__ void load_weight(float* w, const float* __restrict__ 
     copy16(w + i / 32 * W_PITCH + i % 32 * 4, W + i * 4);
   }
 }
+template <int R>
 __device__ __forceinline__ void load_block(float (*rows)[DD], const float* __restrict__ src, int have) {
 #pragma unroll
-  for (int x = 0; x < RB * DD / 4 / R_THREADS; ++x) {
+  for (int x = 0; x < R * DD / 4 / R_THREADS; ++x) {
     const int i = x * R_THREADS + threadIdx.x;
     if (i / 32 < have) copy16(&rows[0][0] + i * 4, src + i * 4);
     else ((float4*)rows)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -839,11 +849,11 @@ __device__ __forceinline__ void load_block(float (*rows)[DD], const float* __res
 }
 
 // out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e], col = 16 warp + lane % 16; in both half-warps
-template <bool kT>
+template <int R, bool kT>
 __device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float* out) {
   const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 4;
 #pragma unroll
-  for (int r = 0; r < RB; ++r) out[r] = 0.f;
+  for (int r = 0; r < R; ++r) out[r] = 0.f;
 #pragma unroll 2
   for (int e = e0; e < DD; e += 8) {
     float4 v;
@@ -851,27 +861,29 @@ __device__ __forceinline__ void rows_product(const float (*rows)[DD], const floa
     else v = make_float4(w[e * W_PITCH + col], w[(e + 1) * W_PITCH + col], w[(e + 2) * W_PITCH + col],
                          w[(e + 3) * W_PITCH + col]);
 #pragma unroll
-    for (int r = 0; r < RB; ++r) {
+    for (int r = 0; r < R; ++r) {
       const float4 x = *(const float4*)&rows[r][e];
       out[r] = fmaf(x.x, v.x, fmaf(x.y, v.y, fmaf(x.z, v.z, fmaf(x.w, v.w, out[r]))));
     }
   }
 #pragma unroll
-  for (int r = 0; r < RB; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
+  for (int r = 0; r < R; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
 }
 // f times the product's column into rows (each half-warp stores half of them)
+template <int R>
 __device__ __forceinline__ void store_column(float (*rows)[DD], const float* v, float f) {
   const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, h = threadIdx.x % 32 / 16;
 #pragma unroll
-  for (int r = 0; r < RB; ++r)
-    if (r / (RB / 2) == h) rows[r][col] = f * v[r];
+  for (int r = 0; r < R; ++r)
+    if (r / (R / 2) == h) rows[r][col] = f * v[r];
 }
 
 // acc[8][8] += sum_r a[r][8 ty ..] b[r][4 tx .. and 64 + 4 tx ..]: a thread's tile of a^T b
+template <int R>
 __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)[DD], float (*acc)[8]) {
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 #pragma unroll 2
-  for (int r = 0; r < RB; ++r) {
+  for (int r = 0; r < R; ++r) {
     const float4 a0 = *(const float4*)&a[r][8 * ty], a1 = *(const float4*)&a[r][8 * ty + 4];
     const float4 b0 = *(const float4*)&b[r][4 * tx], b1 = *(const float4*)&b[r][64 + 4 * tx];
     const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
@@ -913,22 +925,23 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
   float (*a)[DD] = (float (*)[DD])(sm + DD * W_PITCH), (*b)[DD] = a + RB, (*o)[DD] = b + RB;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / RB;
   float v[RB];
+  let_next_start();
   if ((int)blockIdx.x < groups) {
     const int j0 = blockIdx.x * RB;
-    load_block(a, P + (int64_t)j0 * DD, k - j0);
+    load_block<RB>(a, P + (int64_t)j0 * DD, k - j0);
     load_weight(sm, W_Q);
     copies_done();
     __syncthreads();
-    rows_product<false>(a, sm, v);
-    store_column(b, v, 1.f);
+    rows_product<RB, false>(a, sm, v);
+    store_column<RB>(b, v, 1.f);
     __syncthreads();
     load_weight(sm, W_K);
     for (int r = warp; r < RB; r += R_THREADS / 32)
       if (j0 + r < k) *(float4*)(Q + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&b[r][lane * 4];
     copies_done();
     __syncthreads();
-    rows_product<true>(b, sm, v);
-    store_column(o, v, u_scale);
+    rows_product<RB, true>(b, sm, v);
+    store_column<RB>(o, v, u_scale);
     __syncthreads();
     for (int r = warp; r < RB; r += R_THREADS / 32)
       store_split(Uhi, Ulo, (int64_t)(j0 + r) * DD + lane * 4, *(const float4*)&o[r][lane * 4]);
@@ -942,13 +955,13 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     const int have = off[u + 1] > off[u] ? k - j0 : 0;
     const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0;
     __syncthreads();
-    load_block(a, dS + in, have);
-    load_block(b, H + in, have);
+    load_block<RB>(a, dS + in, have);
+    load_block<RB>(b, H + in, have);
     copies_done();
     __syncthreads();
-    rows_product<true>(a, sm, v);
-    store_column(o, v, inv);
-    add_outer(b, a, dwv);
+    rows_product<RB, true>(a, sm, v);
+    store_column<RB>(o, v, inv);
+    add_outer<RB>(b, a, dwv);
     __syncthreads();
     for (int r = warp; r < RB; r += R_THREADS / 32) {
       const float4 x = *(const float4*)&o[r][lane * 4], hv = *(const float4*)&b[r][lane * 4];
@@ -964,7 +977,7 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
   store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
 }
 
-// 16 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
+// 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
 // the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
 __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
                                                                   const float* __restrict__ P,
@@ -974,15 +987,17 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
                                                                   float* __restrict__ part_qk) {
   extern __shared__ __align__(16) float sm[];
   float *w0 = sm, *w1 = sm + DD * W_PITCH;
-  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RB, (*dq)[DD] = q + RB;
+  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float dwq[8][8] = {}, dwk[8][8] = {}, v[RB];
+  float dwq[8][8] = {}, dwk[8][8] = {}, v[RW];
+  let_next_start();
   load_weight(w0, W_K);
   load_weight(w1, W_Q);
-  for (int j0 = blockIdx.x * RB; j0 < k; j0 += gridDim.x * RB) {
+  wait_for_previous();
+  for (int j0 = blockIdx.x * RW; j0 < k; j0 += gridDim.x * RW) {
     __syncthreads();
-    load_block(q, Q + (int64_t)j0 * DD, k - j0);
-    for (int r = warp; r < RB; r += R_THREADS / 32) {
+    load_block<RW>(q, Q + (int64_t)j0 * DD, k - j0);
+    for (int r = warp; r < RW; r += R_THREADS / 32) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       if (j0 + r < k) {
         const float* src = Epart + (int64_t)(j0 + r) * DD + lane * 4;
@@ -996,18 +1011,18 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
     }
     copies_done();
     __syncthreads();
-    rows_product<false>(e, w0, v);
-    store_column(dq, v, rs);
-    add_outer(e, q, dwk);
+    rows_product<RW, false>(e, w0, v);
+    store_column<RW>(dq, v, rs);
+    add_outer<RW>(e, q, dwk);
     __syncthreads();                         // q and e are no longer read: P and dP replace them
-    load_block(q, P + (int64_t)j0 * DD, k - j0);
-    rows_product<true>(dq, w1, v);
-    store_column(e, v, 1.f);
+    load_block<RW>(q, P + (int64_t)j0 * DD, k - j0);
+    rows_product<RW, true>(dq, w1, v);
+    store_column<RW>(e, v, 1.f);
     copies_done();
     __syncthreads();
-    for (int r = warp; r < RB; r += R_THREADS / 32)
+    for (int r = warp; r < RW; r += R_THREADS / 32)
       if (j0 + r < k) *(float4*)(dP + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&e[r][lane * 4];
-    add_outer(q, dq, dwq);
+    add_outer<RW>(q, dq, dwq);
   }
   store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq, 1.f);
   store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk, rs);
@@ -1020,6 +1035,7 @@ __global__ void __launch_bounds__(R_THREADS) tw_sum_kernel(const float* __restri
                                                            float* __restrict__ dW_V, float* __restrict__ dW_Q,
                                                            float* __restrict__ dW_K) {
   __shared__ float4 sums[R_THREADS / 32][32];
+  wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int which = blockIdx.x / DD, at = blockIdx.x % DD * DD + lane * 4;
   const float* src = (which == 0 ? part_v : part_qk + (which - 1) * DD * DD) + at;
@@ -1051,7 +1067,7 @@ Chunking slice_chunks(int64_t n, int k) {
 }
 // CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again)
 int value_parts(int B, int k) { return (int)std::min<int64_t>((int64_t)B * (padded_k(k) / RB), 128); }
-int weight_parts(int k) { return std::min((k + RB - 1) / RB, 64); }
+int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
 
 sa_status map_rows(CUtensorMap* map, const void* base, int64_t rows, uint32_t box_rows) {
@@ -1108,21 +1124,22 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
     if ((s = map_rows(&tmH64, w.Hhi, hrows, 64)) != SA_OK) return s;
     SParams sp{a.off_dev, a.B, w.chE, slices, kp, w.stat_user, w.stat_slot, device_status_word()};
     SA_TIMED("tw_lse_kernel", st,
-             (tw_lse_kernel<<<w.chE.G * slices, S_THREADS, S_SMEM, st>>>(tmX, tmU, tmUlo, sp)));
+             launch_after(tw_lse_kernel, w.chE.G * slices, S_THREADS, S_SMEM, st, tmX, tmU, tmUlo, sp));
     SA_TIMED("tw_lse_combine_kernel", st,
-             (tw_lse_combine_kernel<<<(unsigned)(hrows / 32), 256, 0, st>>>(a.off_dev, w.chE, a.k, kp, w.stat_user,
-                                                                            w.stat_slot, w.lse2)));
+             launch_after(tw_lse_combine_kernel, (unsigned)(hrows / 32), 256, 0, st, a.off_dev, w.chE, a.k, kp, w.stat_user,
+                          w.stat_slot, w.lse2));
     XParams xp{a.off_dev, a.B, w.chX, kp, w.lse2, w.c2, (__nv_bfloat16*)a.dX, device_status_word()};
-    SA_TIMED("tw_dx_kernel", st, (tw_dx_kernel<<<w.chX.G, X_THREADS, X_SMEM, st>>>(tmX, tmU64, tmUlo64, tmH64, xp)));
+    SA_TIMED("tw_dx_kernel", st,
+             launch_after(tw_dx_kernel, w.chX.G, X_THREADS, X_SMEM, st, tmX, tmU64, tmUlo64, tmH64, xp));
     EParams ep{a.off_dev, a.B, w.chE, slices, a.k, kp, w.lse2, w.c, w.Epart, device_status_word()};
     SA_TIMED("tw_e_kernel", st,
-             (tw_e_kernel<<<w.chE.G * slices, E_THREADS, E_SMEM, st>>>(tmX, tmU, tmUlo, tmH, tmHlo, ep)));
+             launch_after(tw_e_kernel, w.chE.G * slices, E_THREADS, E_SMEM, st, tmX, tmU, tmUlo, tmH, tmHlo, ep));
   }
   SA_TIMED("tw_weights_kernel", st,
-           (tw_weights_kernel<<<n_qk, R_THREADS, WEIGHTS_SMEM, st>>>(a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q, a.W_K, a.dP,
-                                                          w.part_qk)));
+           launch_after(tw_weights_kernel, n_qk, R_THREADS, WEIGHTS_SMEM, st, a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q,
+                        a.W_K, a.dP, w.part_qk));
   SA_TIMED("tw_sum_kernel", st,
-           (tw_sum_kernel<<<3 * DD, R_THREADS, 0, st>>>(w.part_v, n_v, inv, w.part_qk, n_qk, a.dW_V, a.dW_Q, a.dW_K)));
+           launch_after(tw_sum_kernel, 3 * DD, R_THREADS, 0, st, w.part_v, n_v, inv, w.part_qk, n_qk, a.dW_V, a.dW_Q, a.dW_K));
   return SA_OK;
 }
 

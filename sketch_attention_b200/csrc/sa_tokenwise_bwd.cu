@@ -19,10 +19,10 @@
 // (per 128 events x 128 prototypes, 512 clocks per product at the bf16 rate):
 //   tw_lse_kernel  row maximum and sum: 2 products; one CTA per (128-prototype
 //     slice, token chunk), lane = prototype, so a row's statistics stay in a thread.
-//   tw_e_kernel    6 products, same split.  [Z; G] = [U; dH] X^T with lane =
+//   e_cta          6 products, same split.  [Z; G] = [U; dH] X^T with lane =
 //     prototype; dZ goes back to TMEM as the A operand of E += dZ X, so nothing
 //     but operands crosses shared memory.
-//   tw_dx_kernel   5 products; one CTA per token chunk, 256 events (two tiles) per
+//   dx_cta         5 products; one CTA per token chunk, 256 events (two tiles) per
 //     pass over the prototypes (halves the prototype traffic out of L2), lane =
 //     token.  The tiles alternate: while one tile's A and dZ are computed the
 //     tensor core works on the other's.  A and dZ overwrite the logits in TMEM.
@@ -338,16 +338,14 @@ struct EParams {
   int* err;
 };
 
-__global__ void __launch_bounds__(E_THREADS, 1)
-    tw_e_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
-                const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH,
-                const __grid_constant__ CUtensorMap tmHlo, EParams p) {
+__device__ __forceinline__ void e_cta(const CUtensorMap& tmX, const CUtensorMap& tmU, const CUtensorMap& tmUlo,
+                                      const CUtensorMap& tmH, const CUtensorMap& tmHlo, const EParams& p, int cta) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   EBars* bars = (EBars*)(smem + E_OFF_BAR);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int sl = blockIdx.x % p.slices, g = blockIdx.x / p.slices;
+  const int sl = cta % p.slices, g = cta / p.slices;
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->u_full, 1);
@@ -599,15 +597,14 @@ struct Units {
   }
 };
 
-__global__ void __launch_bounds__(X_THREADS, 1)
-    tw_dx_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
-                 const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH, XParams p) {
+__device__ __forceinline__ void dx_cta(const CUtensorMap& tmX, const CUtensorMap& tmU, const CUtensorMap& tmUlo,
+                                       const CUtensorMap& tmH, const XParams& p, int cta) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   XBars* bars = (XBars*)(smem + X_OFF_BAR);
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = blockIdx.x, nch = p.kp / KC;
+  const int g = cta, nch = p.kp / KC;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -812,6 +809,21 @@ __global__ void __launch_bounds__(X_THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Both in one launch: CTAs [0, x_ctas) compute dX, the others E.  Neither needs the other; a small
+// call's run side by side, and a large one's E starts on the SMs that finish their dX first.
+static_assert(E_THREADS == X_THREADS, "one launch for both");
+constexpr uint32_t GRADS_SMEM = E_SMEM > X_SMEM ? E_SMEM : X_SMEM;
+
+__global__ void __launch_bounds__(X_THREADS, 1)
+    tw_grads_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
+                    const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH,
+                    const __grid_constant__ CUtensorMap tmHlo, const __grid_constant__ CUtensorMap tmU64,
+                    const __grid_constant__ CUtensorMap tmUlo64, const __grid_constant__ CUtensorMap tmH64,
+                    const __grid_constant__ XParams xp, const __grid_constant__ EParams ep, int x_ctas) {
+  if ((int)blockIdx.x < x_ctas) dx_cta(tmX, tmU64, tmUlo64, tmH64, xp, (int)blockIdx.x);
+  else e_cta(tmX, tmU, tmUlo, tmH, tmHlo, ep, (int)blockIdx.x - x_ctas);
 }
 
 // ============================================================== rows of 128 columns
@@ -1096,11 +1108,10 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
 }
 
 sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st) {
-  static unsigned long long done_s = 0, done_e = 0, done_x = 0, done_p = 0, done_w = 0;
+  static unsigned long long done_s = 0, done_g = 0, done_p = 0, done_w = 0;
   static std::mutex mu;
   set_smem_limit_once((const void*)tw_lse_kernel, S_SMEM, &done_s, mu);
-  set_smem_limit_once((const void*)tw_e_kernel, E_SMEM, &done_e, mu);
-  set_smem_limit_once((const void*)tw_dx_kernel, X_SMEM, &done_x, mu);
+  set_smem_limit_once((const void*)tw_grads_kernel, GRADS_SMEM, &done_g, mu);
   set_smem_limit_once((const void*)tw_prepare_kernel, PREP_SMEM, &done_p, mu);
   set_smem_limit_once((const void*)tw_weights_kernel, WEIGHTS_SMEM, &done_w, mu);
   const int kp = padded_k(a.k), slices = kp / TILE, n_v = value_parts(a.B, a.k), n_qk = weight_parts(a.k);
@@ -1129,11 +1140,10 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
              launch_after(tw_lse_combine_kernel, (unsigned)(hrows / 32), 256, 0, st, a.off_dev, w.chE, a.k, kp, w.stat_user,
                           w.stat_slot, w.lse2));
     XParams xp{a.off_dev, a.B, w.chX, kp, w.lse2, w.c2, (__nv_bfloat16*)a.dX, device_status_word()};
-    SA_TIMED("tw_dx_kernel", st,
-             launch_after(tw_dx_kernel, w.chX.G, X_THREADS, X_SMEM, st, tmX, tmU64, tmUlo64, tmH64, xp));
     EParams ep{a.off_dev, a.B, w.chE, slices, a.k, kp, w.lse2, w.c, w.Epart, device_status_word()};
-    SA_TIMED("tw_e_kernel", st,
-             launch_after(tw_e_kernel, w.chE.G * slices, E_THREADS, E_SMEM, st, tmX, tmU, tmUlo, tmH, tmHlo, ep));
+    SA_TIMED("tw_grads_kernel", st,
+             launch_after(tw_grads_kernel, w.chX.G + w.chE.G * slices, X_THREADS, GRADS_SMEM, st, tmX, tmU, tmUlo, tmH,
+                          tmHlo, tmU64, tmUlo64, tmH64, xp, ep, w.chX.G));
   }
   SA_TIMED("tw_weights_kernel", st,
            launch_after(tw_weights_kernel, n_qk, R_THREADS, WEIGHTS_SMEM, st, a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q,

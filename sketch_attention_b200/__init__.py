@@ -629,22 +629,27 @@ class AdamWTensors:
     def __init__(self, tensors: Sequence[dict]):
         self.tensors = [dict(t) for t in tensors]
         self.c = (AdamWTensorC * max(len(self.tensors), 1))()
-        self.device = self.tensors[0]["param"].device if self.tensors else None
+        self.device = dev = self.tensors[0]["param"].device if self.tensors else None
+        f32, f8 = torch.float32, torch.float8_e4m3fn
+
+        def at(t, name, dtype, size):
+            x = t[name]
+            if not (x.dtype is dtype and x.numel() == size and x.device == dev and x.is_contiguous() and x.is_cuda):
+                _need(name, x if not x.is_contiguous() else x.view(-1), dtype, (size,), dev)
+            return x.data_ptr()
+
         for c, t in zip(self.c, self.tensors):
-            n = t["param"].numel()
-            flat = lambda name: t[name].view(-1) if t[name].is_contiguous() else t[name]  # noqa: E731
-            need = lambda name, dt, size=n: _need(name, flat(name), dt, (size,), self.device).data_ptr()  # noqa: E731
-            c.n, c.weight_decay = n, float(t.get("weight_decay", 0.0))
-            c.param = need("param", torch.float32)
-            c.grad, c.grad_dtype = need("grad", t["grad"].dtype), _dtype_code(t["grad"])
-            if t["m"].dtype == torch.float8_e4m3fn:
+            n, grad = t["param"].numel(), t["grad"].dtype
+            c.n, c.weight_decay = n, t.get("weight_decay", 0.0)
+            c.param, c.grad, c.grad_dtype = at(t, "param", f32, n), at(t, "grad", grad, n), _dtype_code(t["grad"])
+            if t["m"].dtype is f8:
                 blocks = -(-n // ADAMW_BLOCK)
-                c.state, c.m, c.v = SA_STATE_8BIT, need("m", torch.float8_e4m3fn), need("v", torch.float8_e4m3fn)
-                c.m_scale, c.v_scale = need("m_scale", torch.float32, blocks), need("v_scale", torch.float32, blocks)
+                c.state, c.m, c.v = SA_STATE_8BIT, at(t, "m", f8, n), at(t, "v", f8, n)
+                c.m_scale, c.v_scale = at(t, "m_scale", f32, blocks), at(t, "v_scale", f32, blocks)
             else:
-                c.state, c.m, c.v = SA_STATE_F32, need("m", torch.float32), need("v", torch.float32)
+                c.state, c.m, c.v = SA_STATE_F32, at(t, "m", f32, n), at(t, "v", f32, n)
             if t.get("param_bf16") is not None:
-                c.param_bf16 = need("param_bf16", torch.bfloat16)
+                c.param_bf16 = at(t, "param_bf16", torch.bfloat16, n)
 
 
 def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, *, step: int = 0,
@@ -656,17 +661,17 @@ def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
     lib = load()
     if not isinstance(tensors, AdamWTensors):
         tensors = AdamWTensors(tensors)
-    if tensors.device is None:
-        return
     dev = tensors.device
+    if dev is None:
+        return
+    scalars = []
     for name, t, dt in (("step_dev", step_dev, torch.int64), ("lr_dev", lr_dev, torch.float32),
                         ("grad_scale", grad_scale, torch.float32)):
-        if t is not None:
-            _need(name, t.view(-1), dt, (1,), dev)
-    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    cfg = AdamWConfigC(lr, beta1, beta2, eps, step, at(step_dev), at(lr_dev), at(grad_scale))
+        scalars.append(None if t is None else _need(name, t.view(-1), dt, (1,), dev).data_ptr())
+    cfg = AdamWConfigC(lr, beta1, beta2, eps, step, *scalars)
     with _at(dev, stream):
-        _check("sa_adamw_step", lib.sa_adamw_step(tensors.c, len(tensors.tensors), cfg, _raw_stream(dev, stream)))
+        status = lib.sa_adamw_step(tensors.c, len(tensors.tensors), cfg, _raw_stream(dev, stream))
+    _check("sa_adamw_step", status)
 
 
 def sa_gather_events_fused_workspace(n_actions: int, d: int = 128, d_ff: int = 256) -> int:

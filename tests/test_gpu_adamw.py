@@ -234,3 +234,27 @@ def test_binding_refuses_wrong_states(lib):
                 {"param": t["param"].double()}, {"grad": t["grad"].cpu()}):
         with pytest.raises((TypeError, ValueError)):
             lib.AdamWTensors([{**t, **bad}])
+
+
+def test_codes_are_the_rounded_quotients(lib):
+    """The 8-bit codes are those of the IEEE quotient value / scale, over many exponents: the kernel
+    divides by a reciprocal and a residual step."""
+    n = 128 * 4000
+    g = torch.Generator().manual_seed(3)
+    t = _tensor(n, 8)
+    for name in ("m", "v", "m_scale", "v_scale"):
+        t[name].zero_()
+    size = torch.exp2(torch.randint(-60, 20, (n // 128,), generator=g).float()).repeat_interleave(128)
+    t["grad"] = (torch.randn(n, generator=g) * size * torch.exp2(torch.randn(n, generator=g) * 4)).cuda()
+    lib.sa_adamw_step([t], 1e-3, 0.5, 0.75, 1e-8, step=1)
+    m, v = t["grad"] * 0.5, (t["grad"] * t["grad"]) * 0.25      # exact scalings of fp32 values
+    for name, x, floor in (("m", m, False), ("v", v.sqrt(), True)):
+        x = x.view(-1, 128)
+        top = x.abs().amax(1, keepdim=True)
+        scale = torch.where(top >= 2.0 ** -100, top * (torch.ones((), device="cuda") / 448), 0.0)
+        assert torch.equal(scale.view(-1), t[name + "_scale"])
+        y = torch.where(scale > 0, x / torch.where(scale > 0, scale, 1.0), 0.0)
+        if floor:
+            y = torch.where((x > 0) & (scale > 0), y.clamp_min(2.0 ** -9), y)
+        want = y.to(torch.float8_e4m3fn).view(torch.uint8).view(-1)
+        assert torch.equal(want & 0x7F, t[name].view(torch.uint8) & 0x7F)   # but for the sign of zero

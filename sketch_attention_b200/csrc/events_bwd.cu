@@ -40,6 +40,7 @@ constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
+constexpr int kCrossThreads = 512, kCrossWarps = kCrossThreads / 32;
 constexpr int kWindowCtas = 3;               // window CTAs per SM: 16 tables take 64 KB of shared memory each
 constexpr int kFusedActions = 16;            // action tables that the window kernel keeps in shared memory
 
@@ -413,14 +414,20 @@ __device__ __forceinline__ Cols sum_range(const float* __restrict__ part, int64_
   Cols acc = zero_cols();
   if (!in) return acc;
   int64_t v = b;
-  for (; v + 8 <= e; v += 8) {
-    Cols x[8];
+  for (; v + 16 <= e; v += 16) {
+    Cols x[16];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = load_cols(part + (v + q) * pitch);
+    for (int q = 0; q < 16; ++q) x[q] = load_cols(part + (v + q) * pitch);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) add_cols(acc, x[q]);
+    for (int q = 0; q < 16; ++q) add_cols(acc, x[q]);
   }
-  for (; v < e; ++v) add_cols(acc, load_cols(part + v * pitch));
+  if (v < e) {                               // the rest, in one batch too
+    Cols x[15];
+#pragma unroll
+    for (int q = 0; q < 15; ++q) x[q] = v + q < e ? load_cols(part + (v + q) * pitch) : zero_cols();
+#pragma unroll
+    for (int q = 0; q < 15; ++q) add_cols(acc, x[q]);
+  }
   return acc;
 }
 
@@ -431,14 +438,14 @@ __device__ __forceinline__ Cols sum_warps(const Cols& mine, Cols (*part)[32]) {
   part[warp][lane] = mine;
   __syncthreads();
   Cols acc = part[0][lane];
-  for (int w = 1; w < kSumWarps; ++w) add_cols(acc, part[w][lane]);
+  for (int w = 1; w < kCrossWarps; ++w) add_cols(acc, part[w][lane]);
   return acc;
 }
 
 // CTAs [0, action_ctas): the action sums, one action each, from `parts` CTAs' tables.  The others: a
 // warp per window whose last run goes on: the run's sum is last[w] + first[w + 1] + ... up to the
 // window where it ends.  Runs over 32 windows or more are added by the whole CTA.
-__global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32_t* __restrict__ first_key,
+__global__ void __launch_bounds__(kCrossThreads) crossing_rows_kernel(const uint32_t* __restrict__ first_key,
                                                                     const uint32_t* __restrict__ open_key,
                                                                     int64_t windows, int d,
                                                                     const float* __restrict__ first,
@@ -446,21 +453,21 @@ __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32
                                                                     float* __restrict__ d_item, int action_ctas,
                                                                     const float* __restrict__ action_part, int parts,
                                                                     float* __restrict__ d_action) {
-  __shared__ Cols part[kSumWarps][32];
-  __shared__ int64_t long_end[kSumWarps];
+  __shared__ Cols part[kCrossWarps][32];
+  __shared__ int64_t long_end[kCrossWarps];
   wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if ((int)blockIdx.x < action_ctas) {
     const int a = (int)blockIdx.x;
     for (int c0 = 0; c0 < d; c0 += 128) {
       const int c = c0 + lane * 4;
-      const Cols acc = sum_warps(sum_range(action_part + (int64_t)a * d + c, (int64_t)parts * warp / kSumWarps,
-                                           (int64_t)parts * (warp + 1) / kSumWarps, (int64_t)action_ctas * d, c < d), part);
+      const Cols acc = sum_warps(sum_range(action_part + (int64_t)a * d + c, (int64_t)parts * warp / kCrossWarps,
+                                           (int64_t)parts * (warp + 1) / kCrossWarps, (int64_t)action_ctas * d, c < d), part);
       if (warp == 0 && c < d) store_cols(d_action + (int64_t)a * d + c, acc);
     }
     return;
   }
-  const int64_t w0 = (int64_t)(blockIdx.x - action_ctas) * kSumWarps, w = w0 + warp;
+  const int64_t w0 = (int64_t)(blockIdx.x - action_ctas) * kCrossWarps, w = w0 + warp;
   const uint32_t run = w + 1 < windows ? open_key[w] : kNone;
   int64_t end = 0;                                   // one behind the last window of the run (0: none to add)
   bool is_long = false;
@@ -490,14 +497,14 @@ __global__ void __launch_bounds__(kSumThreads) crossing_rows_kernel(const uint32
       store_cols(d_item + (int64_t)run * d + c, acc);
     }
   __syncthreads();
-  for (int i = 0; i < kSumWarps; ++i) {
+  for (int i = 0; i < kCrossWarps; ++i) {
     const int64_t e = long_end[i], b = w0 + i;
     if (e == 0) continue;
     const int64_t cnt = e - b - 1;
     const uint32_t key = open_key[b];
     for (int c0 = 0; c0 < d; c0 += 128) {
       const int c = c0 + lane * 4;
-      Cols acc = sum_range(first + c, b + 1 + cnt * warp / kSumWarps, b + 1 + cnt * (warp + 1) / kSumWarps, d, c < d);
+      Cols acc = sum_range(first + c, b + 1 + cnt * warp / kCrossWarps, b + 1 + cnt * (warp + 1) / kCrossWarps, d, c < d);
       if (warp == 0 && c < d) add_cols(acc, load_cols(last + b * d + c));
       acc = sum_warps(acc, part);
       if (warp == 0 && c < d) store_cols(d_item + (int64_t)key * d + c, acc);
@@ -620,7 +627,8 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
   }
   const int ac = d_action ? n_actions : 0;
   SA_TIMED("crossing_rows_kernel", st,
-           launch_after(crossing_rows_kernel, ac + (d_item ? window_ctas : 0), kSumThreads, 0, st, w.first_key, w.open_key,
+           launch_after(crossing_rows_kernel, ac + (d_item ? (int)((windows + kCrossWarps - 1) / kCrossWarps) : 0),
+                        kCrossThreads, 0, st, w.first_key, w.open_key,
                         windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action));
   return SA_OK;
 }

@@ -271,6 +271,15 @@ def _raw_stream(device, stream) -> int:
     return _current_raw_stream(device.index)
 
 
+def _used_on(stream, *ts):
+    """Tensors of the caller that a call on `stream` uses: the allocator keeps their memory until that
+    work is done, although the caller may drop them as soon as the call returns."""
+    if stream is not None:
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _workspace(given: Optional[torch.Tensor], size: int, device) -> torch.Tensor:
     """The caller's workspace if it is large enough, else a new one (at least one byte)."""
     if given is None:
@@ -397,6 +406,7 @@ def sa_backward_tokenwise(X: torch.Tensor, offsets, P, W_Q, W_K, W_V, eps: float
                                        *(t.data_ptr() for t in res.values()), ws.data_ptr(), ws.nbytes,
                                        _raw_stream(dev, stream))
         _check("sa_backward_tokenwise", st)
+    _used_on(stream, X, P, W_Q, W_K, W_V, H, dS, offsets_dev, workspace, *res.values())
     return res
 
 
@@ -616,6 +626,7 @@ def sa_gather_events_backward(item_ids: torch.Tensor, action_ids: torch.Tensor, 
                                            None if action is None else action.data_ptr(), ws.data_ptr(), ws.nbytes,
                                            _raw_stream(dev, stream))
         _check("sa_gather_events_backward", st)
+    _used_on(stream, item_ids, action_ids, dX, workspace, *res.values())
     return res
 
 
@@ -672,6 +683,8 @@ def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
     with _at(dev, stream):
         status = lib.sa_adamw_step(tensors.c, len(tensors.tensors), cfg, _raw_stream(dev, stream))
     _check("sa_adamw_step", status)
+    _used_on(stream, step_dev, lr_dev, grad_scale, *(x for t in tensors.tensors for x in t.values()
+                                                      if isinstance(x, torch.Tensor)))
 
 
 def sa_gather_events_fused_workspace(n_actions: int, d: int = 128, d_ff: int = 256) -> int:

@@ -119,3 +119,30 @@ def test_the_same_bits_twice_captured_and_only_the_outputs_written(lib):
         assert torch.equal(first[name], out[name]) and torch.equal(first[name], other[name])
     assert bool((item[-guard:] == 7.0).all()) and bool((action[-guard:] == 7.0).all())
     assert bool((ws[size:] == 0x5A).all())
+
+
+def test_two_calls_at_once(lib):
+    a = _inputs(60_000, 5000, 8, 128, torch.bfloat16, 8)
+    b = _inputs(90_000, 700, 16, 128, torch.float32, 9)
+    alone = [lib.sa_gather_events_backward(*a, 5000, 8), lib.sa_gather_events_backward(*b, 700, 16)]
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        got.append(lib.sa_gather_events_backward(*a, 5000, 8, stream=s))
+        got.append(lib.sa_gather_events_backward(*b, 700, 16, stream=t))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert all(torch.equal(g[k], alone[i % 2][k]) for k in g)
+
+
+def test_a_gradient_that_is_not_finite_stays_in_its_rows(lib):
+    ids, acts, dX = _inputs(5000, 300, 8, 128, torch.float32, 10)
+    clean = lib.sa_gather_events_backward(ids, acts, dX, 300, 8)
+    dX[1234] = float("nan")
+    got = lib.sa_gather_events_backward(ids, acts, dX, 300, 8)
+    torch.cuda.synchronize()
+    for name, row in (("d_item", int(ids[1234])), ("d_action", int(acts[1234]))):
+        assert bool(got[name][row].isnan().all())
+        keep = torch.arange(len(got[name]), device="cuda") != row
+        assert torch.equal(got[name][keep], clean[name][keep])

@@ -111,7 +111,8 @@ def _problem(lengths, k, ps=1.0, seed=60):
 CASES = [
     ((1,), 1, 1.0), ((2,), 3, 1.0), ((128,), 128, 1.0), ((129,), 129, 2.0), ((256, 257), 64, 1.0),
     ((130, 0, 700, 5, 1), 100, 1.0), ((0, 0, 3), 65, 1.0), ((1, 2000), 200, 4.0), ((5000,), 300, 0.25),
-    ((300,) * 7, 384, 1.0), ((37000, 20), 40, 1.0), ((1100, 1024, 1023), 1024, 2.0),
+    ((300,) * 7, 384, 1.0), ((37000, 20), 40, 1.0), ((1100, 1024, 1023), 1024, 2.0), ((700, 257), 4096, 1.0),
+    ((2,) * 40, 600, 2.0),
 ]
 
 
@@ -209,3 +210,33 @@ def test_captured_and_on_another_stream(lib):
         assert torch.equal(eager[name], other[name]), name
         assert torch.equal(want[name], held[name]), name
     lib.poll_device_status()
+
+
+def test_two_calls_at_once(lib):
+    """Calls on two streams, each with its own buffers, do not disturb one another, nor does it matter
+    that a call's offsets are dropped (and their memory handed out again) while its kernels run."""
+    problems = [_problem((3000, 500), 256, seed=70), _problem((200, 0, 4100), 512, seed=71)]
+    inputs = [(p, dS, sa_device_inputs(p)) for p, dS in problems]
+    alone = [_run(lib, p, dS, dv) for p, dS, dv in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in problems]
+    got = []
+    for _ in range(3):
+        for s, (p, dS, dv), (_, H) in zip(streams, inputs, alone):
+            got.append(_run(lib, p, dS, dv, H=H, stream=s, offsets_dev=torch.from_numpy(p.offsets).cuda())[0])
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for name in NAMES:
+            assert torch.equal(g[name], alone[i % 2][0][name]), name
+
+
+def test_h_of_users_without_events_is_not_read(lib):
+    p, dS = _problem((50, 0, 30), 100)
+    clean, H = _run(lib, p, dS)
+    H = H.clone()
+    H[1] = float("nan")
+    dS[1] = float("nan")
+    got, _ = _run(lib, p, dS, H=H)
+    torch.cuda.synchronize()
+    for name in NAMES:
+        assert torch.equal(clean[name], got[name]), name

@@ -543,9 +543,9 @@ typedef struct {
 
 typedef struct {
   double lr, beta1, beta2, eps;
-  int64_t step;                 /* t >= 1 of this step (unless step_dev) */
+  int64_t step;                 /* t of this step, >= 1 (unused with step_dev) */
   /* Optional device scalars, read when the kernel runs, so that a captured step can be
-   * replayed with new values: t, lr, and a factor on every gradient (a clipping
+   * replayed with new values: t (>= 1), lr, and a factor on every gradient (a clipping
    * coefficient or the inverse of a loss scale).  NULL: step, lr, 1.  A grad_scale that
    * is not finite leaves every tensor as it is. */
   const int64_t* step_dev;

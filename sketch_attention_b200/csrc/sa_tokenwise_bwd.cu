@@ -1077,8 +1077,12 @@ int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
 Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
-// CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again)
-int value_parts(int B, int k) { return (int)std::min<int64_t>((int64_t)B * (padded_k(k) / RB), 128); }
+// CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again):
+// up to 128 take a block of rows or two each, more (two per SM) only where there are many blocks
+int value_parts(int B, int k) {
+  const int64_t blocks = (int64_t)B * (padded_k(k) / RB), most = 2 * device_info().sm_count;
+  return (int)std::min(blocks, std::max<int64_t>(128, std::min(blocks / 4, most)));
+}
 int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
 

@@ -893,7 +893,7 @@ __device__ __forceinline__ void store_column(float (*rows)[DD], const float* v, 
 // acc[8][8] += sum_r a[r][8 ty ..] b[r][4 tx .. and 64 + 4 tx ..]: a thread's tile of a^T b
 template <int R>
 __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)[DD], float (*acc)[8]) {
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int ty = threadIdx.x / 16 % 16, tx = threadIdx.x % 16;
 #pragma unroll 2
   for (int r = 0; r < R; ++r) {
     const float4 a0 = *(const float4*)&a[r][8 * ty], a1 = *(const float4*)&a[r][8 * ty + 4];
@@ -907,7 +907,7 @@ __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)
   }
 }
 __device__ __forceinline__ void store_outer(float* __restrict__ part, const float (*acc)[8], float f) {
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int ty = threadIdx.x / 16 % 16, tx = threadIdx.x % 16;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float* dst = part + (8 * ty + i) * DD + 4 * tx;
@@ -925,7 +925,7 @@ __device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo
 }
 
 // CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others, 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
+// The others (where the rows are few), 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
 // (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
 __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
@@ -987,6 +987,100 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     }
   }
   store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
+}
+
+// The same dH, c and parts of sum H^T dS where there are many rows (many users), 64 rows a step with the
+// next step's on their way: warps 0-7 take dH, a 4 x 8 tile a thread (12 shared loads of 16 bytes
+// for 128 FMA, where tw_prepare_kernel's column a thread takes 17 for 64), warps 8-15 the outer products.
+// Every CTA has a first step: the grid is no larger than the number of steps.
+constexpr int V_ROWS = 64, V_THREADS = 512;
+constexpr uint32_t VALUES_SMEM = W_BYTES + 4 * V_ROWS * ROW_BYTES;
+
+__global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
+    const int64_t* __restrict__ off, int B, int k, int kp, float inv, const float* __restrict__ W_V,
+    const float* __restrict__ dS, const float* __restrict__ H, __nv_bfloat16* __restrict__ Hhi,
+    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v) {
+  extern __shared__ __align__(16) float sm[];
+  using Rows = float (*)[DD];
+  const Rows rows = (Rows)(sm + DD * W_PITCH);            // dS, H of this step, dS, H of the next
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / V_ROWS;
+  const int64_t blocks = (int64_t)B * groups;
+  auto load = [&](int64_t g, int s) {
+    const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS;
+    const int have = off[u + 1] > off[u] ? k - j0 : 0;
+    const int64_t in = ((int64_t)u * k + j0) * DD;
+#pragma unroll
+    for (int x = 0; x < V_ROWS * DD / 4 / V_THREADS; ++x) {
+      const int i = x * V_THREADS + threadIdx.x;
+      float *a = &rows[2 * s * V_ROWS][0] + i * 4, *b = a + V_ROWS * DD;
+      if (i / 32 < have) {
+        copy16(a, dS + in + i * 4);
+        copy16(b, H + in + i * 4);
+      } else {
+        *(float4*)a = *(float4*)b = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+  };
+  let_next_start();
+  for (int i = threadIdx.x; i < DD * DD / 4; i += V_THREADS) copy16(sm + i / 32 * W_PITCH + i % 32 * 4, W_V + i * 4);
+  load(blockIdx.x, 0);
+  float acc[8][8] = {};
+  int s = 0;
+  for (int64_t g = blockIdx.x; g < blocks; g += gridDim.x, s ^= 1) {
+    copies_done();
+    __syncthreads();
+    if (g + gridDim.x < blocks) load(g + gridDim.x, s ^ 1);
+    const Rows a = rows + 2 * s * V_ROWS, b = a + V_ROWS;
+    if (warp >= 8) {
+      add_outer<V_ROWS>(b, a, acc);
+      continue;
+    }
+    // rows r0 .. r0 + 3, columns x0 + 16 j
+    const int r0 = 8 * warp + lane / 16 * 4, x0 = lane % 16;
+    const int64_t row0 = g / groups * kp + g % groups * V_ROWS + r0;
+    float v[4][8] = {};
+#pragma unroll 2
+    for (int e = 0; e < DD; e += 4) {
+      float4 x[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = *(const float4*)&a[r0 + r][e];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float4 w = *(const float4*)(sm + (x0 + 16 * j) * W_PITCH + e);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[r][j] = fmaf(x[r].x, w.x, fmaf(x[r].y, w.y, fmaf(x[r].z, w.z, fmaf(x[r].w, w.w, v[r][j]))));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[r][j] *= inv;
+        dot = fmaf(v[r][j], b[r0 + r][x0 + 16 * j], dot);
+      }
+      for (int m = 8; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+      if (x0 == 0) {
+        cj[row0 + r] = dot;
+        c2[row0 + r] = kLn2 * dot;
+      }
+      // neighbours exchange columns: an even lane has (x0, x0 + 1) of 16 j, an odd one (x0 - 1, x0) of 16 (j + 1)
+      const bool odd = x0 & 1;
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[r][j] : v[r][j + 1], 1);
+        const float first = odd ? got : v[r][j], second = odd ? v[r][j + 1] : got;
+        const int64_t at = (row0 + r) * DD + 16 * (j + odd) + (x0 & ~1);
+        uint32_t hi, lo;
+        split2(first, second, hi, lo);
+        *(uint32_t*)(Hhi + at) = hi;
+        *(uint32_t*)(Hlo + at) = lo;
+      }
+    }
+  }
+  if (warp >= 8) store_outer(part_v + (int64_t)blockIdx.x * DD * DD, acc, 1.f);
+  wait_for_previous();                       // so that what follows this kernel follows U's too
 }
 
 // 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
@@ -1077,11 +1171,14 @@ int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
 Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
-// CTAs of the row kernels that keep a part of a d x d gradient each (64 KB written and read again):
-// up to 128 take a block of rows or two each, more (two per SM) only where there are many blocks
+// whether the rows of dS are many enough for tw_values_kernel: a step for half of the SMs.  A call's
+// time with tw_prepare_kernel alone and with it (us): 1 user x 1024 prototypes 75.9, 86.2; 32 x 128 64.5,
+// 69.4; 5 x 1024 131, 123; 12 x 512 98.5, 84.3; 64 x 1024 354, 319; 512 x 1024 1780, 1593
+bool many_rows(int B, int k) { return (int64_t)B * (padded_k(k) / V_ROWS) >= device_info().sm_count / 2; }
+// CTAs that keep a part of the d x d gradient of W_V each (64 KB written and read again)
 int value_parts(int B, int k) {
-  const int64_t blocks = (int64_t)B * (padded_k(k) / RB), most = 2 * device_info().sm_count;
-  return (int)std::min(blocks, std::max<int64_t>(128, std::min(blocks / 4, most)));
+  const int64_t rows = (int64_t)B * padded_k(k);
+  return (int)(many_rows(B, k) ? std::min<int64_t>(rows / V_ROWS, device_info().sm_count) : std::min<int64_t>(rows / RB, 128));
 }
 int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }
@@ -1112,20 +1209,26 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
 }
 
 sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& w, cudaStream_t st) {
-  static unsigned long long done_s = 0, done_g = 0, done_p = 0, done_w = 0;
+  static unsigned long long done_s = 0, done_g = 0, done_p = 0, done_w = 0, done_v = 0;
   static std::mutex mu;
   set_smem_limit_once((const void*)tw_lse_kernel, S_SMEM, &done_s, mu);
   set_smem_limit_once((const void*)tw_grads_kernel, GRADS_SMEM, &done_g, mu);
   set_smem_limit_once((const void*)tw_prepare_kernel, PREP_SMEM, &done_p, mu);
+  set_smem_limit_once((const void*)tw_values_kernel, VALUES_SMEM, &done_v, mu);
   set_smem_limit_once((const void*)tw_weights_kernel, WEIGHTS_SMEM, &done_w, mu);
   const int kp = padded_k(a.k), slices = kp / TILE, n_v = value_parts(a.B, a.k), n_qk = weight_parts(a.k);
+  const bool many = many_rows(a.B, a.k);
   const float inv = 1.f / (1.f + a.eps);                // m = 1 for a user with events
   const float rs = 1.f / sqrtf((float)a.d);
   sa_status s;
   SA_TIMED("tw_prepare_kernel", st,
-           (tw_prepare_kernel<<<kp / RB + n_v, R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
+           (tw_prepare_kernel<<<kp / RB + (many ? 0 : n_v), R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
                                                                    a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi, w.Ulo,
                                                                    w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
+  if (many)
+    SA_TIMED("tw_values_kernel", st,
+             launch_after(tw_values_kernel, n_v, V_THREADS, VALUES_SMEM, st, a.off_dev, a.B, a.k, kp, inv, a.W_V, a.dS, a.H,
+                          w.Hhi, w.Hlo, w.c, w.c2, w.part_v));
   if (a.n_total > 0) {
     CUtensorMap tmX, tmU, tmUlo, tmH, tmHlo, tmU64, tmUlo64, tmH64;
     const int64_t hrows = (int64_t)a.B * kp;

@@ -6,7 +6,8 @@ is no CPU fallback: if the library is missing or a call fails, an exception
 is raised.
 
 Entry points keep the C names: ``sa_forward``, ``sa_backward``,
-``stca_forward``, ``stca_forward_full``, ``stca_fuse`` (plus the workspace queries).
+``stca_forward``, ``stca_forward_full``, ``stca_fuse`` and the others of the header (plus the
+workspace queries); ``AdamWTensors`` describes the tensors of ``sa_adamw_step``.
 """
 from __future__ import annotations
 
@@ -617,7 +618,7 @@ def sa_gather_events_backward(item_ids: torch.Tensor, action_ids: torch.Tensor, 
             if t is not None:
                 res[name] = _need(name, t, torch.float32, (rows, d), dev)
             elif want:
-                res[name] = torch.empty(rows, d, device=dev)
+                res[name] = torch.empty(rows, d, dtype=torch.float32, device=dev)
         ws = _workspace(workspace, lib.sa_gather_events_backward_workspace(n, vocab, n_actions, d), dev)
         item, action = res.get("d_item"), res.get("d_action")
         st = lib.sa_gather_events_backward(item_ids.data_ptr(), action_ids.data_ptr(), n, dX.data_ptr(),
@@ -635,7 +636,8 @@ class AdamWTensors:
     "param" (fp32), "grad" (fp32 or bf16), "m" and "v" (both fp32, or both float8_e4m3fn with
     "m_scale" and "v_scale", fp32, one value per ADAMW_BLOCK values), all of one size and device;
     optionally "param_bf16" (bf16, receives the rounded parameter) and "weight_decay" (default 0).
-    The arrays are held by reference: a step reads and updates them in place."""
+    The arrays are held by reference: a step reads and updates them in place.  No array that a step
+    writes may be in the list twice (two blocks of threads would update it at once): ValueError."""
 
     def __init__(self, tensors: Sequence[dict]):
         self.tensors = [dict(t) for t in tensors]
@@ -649,6 +651,11 @@ class AdamWTensors:
                 _need(name, x if not x.is_contiguous() else x.view(-1), dtype, (size,), dev)
             return x.data_ptr()
 
+        written = [t[name].data_ptr() for t in self.tensors for name in ("param", "m", "v", "m_scale", "v_scale",
+                                                                         "param_bf16")
+                   if t.get(name) is not None and t[name].numel() > 0]
+        if len(set(written)) < len(written):
+            raise ValueError("an array that the step writes is in the list twice")
         for c, t in zip(self.c, self.tensors):
             n, grad = t["param"].numel(), t["grad"].dtype
             c.n, c.weight_decay = n, t.get("weight_decay", 0.0)

@@ -258,3 +258,30 @@ def test_codes_are_the_rounded_quotients(lib):
             y = torch.where((x > 0) & (scale > 0), y.clamp_min(2.0 ** -9), y)
         want = y.to(torch.float8_e4m3fn).view(torch.uint8).view(-1)
         assert torch.equal(want & 0x7F, t[name].view(torch.uint8) & 0x7F)   # but for the sign of zero
+
+
+def test_an_array_twice_in_the_list_is_refused(lib):
+    a, b = _tensor(300, 8), _tensor(300, 8, seed=1)
+    for name in ("param", "m", "v", "m_scale"):
+        with pytest.raises(ValueError):
+            lib.AdamWTensors([a, {**b, name: a[name]}])
+    lib.AdamWTensors([a, {**b, "grad": a["grad"]}, _tensor(0, 32), _tensor(0, 32)])
+
+
+def test_gradients_dropped_while_a_step_on_another_stream_runs(lib):
+    """Their memory is not handed out again before the step has read it."""
+    want, got = [_tensor(8_000_000, 32, seed=2)], [_tensor(8_000_000, 32, seed=2)]
+    lib.sa_adamw_step(want, step=1, **HYPER)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    held = dict(got[0])
+    del got[0]["grad"]
+    step = [held]
+    lib.sa_adamw_step([_tensor(30_000_000, 32, seed=3)], step=1, stream=stream, **HYPER)   # keeps the stream busy
+    lib.sa_adamw_step(step, step=1, stream=stream, **HYPER)
+    del step, held
+    for _ in range(3):
+        torch.full((8_000_000,), float("nan"), device="cuda")
+    torch.cuda.synchronize()
+    for name in ("param", "m", "v"):
+        assert torch.equal(got[0][name], want[0][name])

@@ -146,3 +146,14 @@ def test_a_gradient_that_is_not_finite_stays_in_its_rows(lib):
         assert bool(got[name][row].isnan().all())
         keep = torch.arange(len(got[name]), device="cuda") != row
         assert torch.equal(got[name][keep], clean[name][keep])
+
+
+def test_the_default_dtype_does_not_matter(lib):
+    x = _inputs(3000, 200, 4, 64, torch.bfloat16, 11)
+    want = lib.sa_gather_events_backward(*x, 200, 4)
+    torch.set_default_dtype(torch.float64)
+    try:
+        got = lib.sa_gather_events_backward(*x, 200, 4)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert all(got[k].dtype == torch.float32 and torch.equal(got[k], want[k]) for k in want)

@@ -690,8 +690,9 @@ def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, 
     with _at(dev, stream):
         status = lib.sa_adamw_step(tensors.c, len(tensors.tensors), cfg, _raw_stream(dev, stream))
     _check("sa_adamw_step", status)
-    _used_on(stream, step_dev, lr_dev, grad_scale, *(x for t in tensors.tensors for x in t.values()
-                                                      if isinstance(x, torch.Tensor)))
+    if stream is not None:                                   # hundreds of tensors: not for nothing
+        _used_on(stream, step_dev, lr_dev, grad_scale, *(x for t in tensors.tensors for x in t.values()
+                                                          if isinstance(x, torch.Tensor)))
 
 
 def sa_gather_events_fused_workspace(n_actions: int, d: int = 128, d_ff: int = 256) -> int:

@@ -73,6 +73,7 @@ __device__ constexpr uint32_t kstep(int ks) { return ((ks >> 2) * 16384 + (ks & 
 __device__ __forceinline__ uint32_t mnmajor(uint32_t addr) { return desc_lo(addr, 16384); }
 __device__ constexpr uint32_t mnstep(int ks) { return ks * 2048 >> 4; }
 
+__device__ __forceinline__ float round_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 // x = hi + lo as bf16 pairs
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf16x2(a, b);
@@ -925,8 +926,10 @@ __device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo
 }
 
 // CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others (where the rows are few), 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = dH . H and ln2 c
-// (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
+// The others (where the rows are few), 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = (hi + lo) . H
+// and c2 = ln2 hi . H (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
+// G - c is small beside G where a softmax has one large weight (x is near H there), so each c is that of
+// the dH which its kernel's G has, hi + lo in E and hi in dX: the rest then costs rest (x - H), not rest x.
 __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, float u_scale, const float* __restrict__ P,
     const float* __restrict__ W_Q, const float* __restrict__ W_K, const float* __restrict__ W_V,
@@ -977,11 +980,17 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     __syncthreads();
     for (int r = warp; r < RB; r += R_THREADS / 32) {
       const float4 x = *(const float4*)&o[r][lane * 4], hv = *(const float4*)&b[r][lane * 4];
-      float dot = fmaf(x.x, hv.x, fmaf(x.y, hv.y, fmaf(x.z, hv.z, x.w * hv.w)));
-      for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+      const float4 hi = make_float4(round_bf16(x.x), round_bf16(x.y), round_bf16(x.z), round_bf16(x.w));
+      float dot_hi = fmaf(hi.x, hv.x, fmaf(hi.y, hv.y, fmaf(hi.z, hv.z, hi.w * hv.w)));
+      float dot = fmaf(round_bf16(x.x - hi.x), hv.x, fmaf(round_bf16(x.y - hi.y), hv.y,
+                  fmaf(round_bf16(x.z - hi.z), hv.z, fmaf(round_bf16(x.w - hi.w), hv.w, dot_hi))));
+      for (int s = 16; s > 0; s >>= 1) {
+        dot += __shfl_xor_sync(0xffffffffu, dot, s);
+        dot_hi += __shfl_xor_sync(0xffffffffu, dot_hi, s);
+      }
       if (lane == 0) {
         cj[row0 + r] = dot;
-        c2[row0 + r] = kLn2 * dot;
+        c2[row0 + r] = kLn2 * dot_hi;
       }
       store_split(Hhi, Hlo, (row0 + r) * DD + lane * 4, x);
     }
@@ -1054,16 +1063,22 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float dot = 0.f;
+      float dot = 0.f, dot_hi = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        const float h = b[r0 + r][x0 + 16 * j];
         v[r][j] *= inv;
-        dot = fmaf(v[r][j], b[r0 + r][x0 + 16 * j], dot);
+        const float hi = round_bf16(v[r][j]);
+        dot_hi = fmaf(hi, h, dot_hi);
+        dot = fmaf(hi, h, fmaf(round_bf16(v[r][j] - hi), h, dot));
       }
-      for (int m = 8; m > 0; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+      for (int m = 8; m > 0; m >>= 1) {
+        dot += __shfl_xor_sync(0xffffffffu, dot, m);
+        dot_hi += __shfl_xor_sync(0xffffffffu, dot_hi, m);
+      }
       if (x0 == 0) {
         cj[row0 + r] = dot;
-        c2[row0 + r] = kLn2 * dot;
+        c2[row0 + r] = kLn2 * dot_hi;
       }
       // neighbours exchange columns: an even lane has (x0, x0 + 1) of 16 j, an odd one (x0 - 1, x0) of 16 (j + 1)
       const bool odd = x0 & 1;

@@ -13,7 +13,8 @@ element against the sums of absolute terms that the oracle's values give:
   truncating 2^-23, + fp32 sums of the drained parts (n / 1024 + 150 terms, 2^-24 each).
 * dP, dW_Q, dW_K: |E_err| through the fp32 projections (three of K <= max(k, 128) terms).
 * dX is one bf16 rounding (2^-8) of A^T dH + dZ^T U, whose operands A, dH, dZ, U are bf16 (2^-8
-  each) and G there takes a bf16 dH (2^-8 g_abs)."""
+  each); G and c there take a bf16 dH (2^-8 (g_abs + |dH| |H|)).  E's take dH as hi + lo, c too
+  (2^-16 |dH| |H|)."""
 import math
 
 import numpy as np
@@ -60,7 +61,8 @@ def _check(lib, p, got, H, dS):
         dH = dS[u] @ WV.T / (1 + p.eps)
         dH_err = 150 * F32 * (np.abs(dS[u]) @ np.abs(WV.T))
         c = (dH * H[u]).sum(1, keepdims=True)
-        c_err = (130 * F32 * np.abs(dH) * np.abs(H[u]) + dH_err * np.abs(H[u])).sum(1, keepdims=True)
+        c_abs = (np.abs(dH) * np.abs(H[u])).sum(1, keepdims=True)
+        c_err = (130 * F32 + 2.0 ** -16) * c_abs + (dH_err * np.abs(H[u])).sum(1, keepdims=True)
         dz = KZ * (np.abs(U) @ ax.T) + U_err @ ax.T
         A_err = A * np.minimum(dz + dz.max(1, keepdims=True) + 2.0 ** -20, 1)
         g, g_abs = dH @ xu.T, np.abs(dH) @ ax.T
@@ -70,7 +72,7 @@ def _check(lib, p, got, H, dS):
         s = 2.0 ** -16 + 128 * 2.0 ** -23 + (n / 1024 + 150) * F32
         E_err += (dZ_err + s * np.abs(dZ)) @ ax
         low = BF + 2.0 ** -12                                                 # bf16, and the fp32 sums' own
-        dZ_low = A * BF * g_abs + dZ_err + low * np.abs(A * (g - c))
+        dZ_low = A * BF * (g_abs + c_abs) + dZ_err + low * np.abs(A * (g - c))
         dX_err[lo:hi] = (A_err + 2 * low * A).T @ np.abs(dH) + dZ_low.T @ np.abs(U) + low * np.abs(dZ).T @ np.abs(U)
         dWV_err += (p.B * k + 40) * F32 * (np.abs(H[u]).T @ np.abs(dS[u]))
     ref = oracle.sa_backward_tokenwise(x, p.offsets, P, WQ, WK, WV, p.eps, dS, H=H)

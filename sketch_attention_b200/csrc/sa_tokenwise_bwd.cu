@@ -1003,103 +1003,217 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
   store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
 }
 
-// The same dH, c and parts of sum H^T dS where there are many rows (many users), 64 rows a step with the
-// next step's on their way: warps 0-7 take dH, a 4 x 8 tile a thread (12 shared loads of 16 bytes
-// for 128 FMA, where tw_prepare_kernel's column a thread takes 17 for 64), warps 8-15 the outer products.
-// Every CTA has a first step: the grid is no larger than the number of steps.
-constexpr int V_ROWS = 64, V_THREADS = 512;
-constexpr uint32_t VALUES_SMEM = W_BYTES + 4 * V_ROWS * ROW_BYTES;
+// The same dH, c, c2 and parts of sum H^T dS where there are many rows (many users), on the tensor
+// cores in fp32 grade: dS, H and W_V as three bf16 parts each (24 bits), six products of the parts, the
+// small ones first (the accumulation truncates at the size of the sum).  64 rows a step:
+//   dH^T = W_V dS^T (lane = column of dH, 64 TMEM columns, two buffers),
+//   dW_V += H^T dS  (K = the rows; the large product and the small ones in accumulators of their own,
+//   which leave TMEM every kVDrain steps and are summed in registers, rounded to nearest).
+// 16 warps split a step's rows into shared memory, then write the step before while the tensor core
+// works (3840 clocks) and the next rows are on their way.  Every CTA has a first step: the grid is
+// no larger than the number of steps.
+constexpr int V_ROWS = 64, V_THREADS = 544, kVDrain = 8;
+constexpr uint32_t VS_BYTES = V_ROWS * DD * 2;                   // a part of a step's dS or H
+constexpr uint32_t V_OFF_S = 3 * XT_BYTES, V_OFF_H = V_OFF_S + 3 * VS_BYTES, V_OFF_RED = V_OFF_H + 3 * VS_BYTES;
+constexpr uint32_t V_OFF_BAR = V_OFF_RED + 2 * 2 * 4 * V_ROWS * 4;
+constexpr uint32_t VALUES_SMEM = V_OFF_BAR + 64 + 1024;
+constexpr uint32_t V_TM_DW = 128, V_TM_DW_LOW = 256;             // dH: columns 0-63 and 64-127
+
+struct VBars {
+  uint64_t full, done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// four columns of a row (c4: which four) as three bf16 parts, into swizzled tiles of 64-column halves
+__device__ __forceinline__ void store_parts(uint32_t base, uint32_t part_bytes, int row, int c4, float4 x) {
+  const uint32_t at = base + (c4 >> 4) * (part_bytes / 2) + row * 128 + ((((c4 & 15) >> 1) ^ (row & 7)) << 4) + (c4 & 1) * 8;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t a = pack_bf16x2(x.x, x.y), b = pack_bf16x2(x.z, x.w);
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + i * part_bytes), "r"(a), "r"(b) : "memory");
+    x.x -= __uint_as_float(a << 16); x.y -= __uint_as_float(a & 0xFFFF0000u);
+    x.z -= __uint_as_float(b << 16); x.w -= __uint_as_float(b & 0xFFFF0000u);
+  }
+}
 
 __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, const float* __restrict__ W_V,
     const float* __restrict__ dS, const float* __restrict__ H, __nv_bfloat16* __restrict__ Hhi,
-    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v) {
-  extern __shared__ __align__(16) float sm[];
-  using Rows = float (*)[DD];
-  const Rows rows = (Rows)(sm + DD * W_PITCH);            // dS, H of this step, dS, H of the next
+    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v, int* err) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  VBars* bars = (VBars*)(smem + V_OFF_BAR);
+  float* red = (float*)(smem + V_OFF_RED);                       // [buffer][c2, c][quarter of the columns][row]
+  volatile int* abort = &bars->abort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / V_ROWS;
-  const int64_t blocks = (int64_t)B * groups;
-  auto load = [&](int64_t g, int s) {
-    const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS;
-    const int have = off[u + 1] > off[u] ? k - j0 : 0;
-    const int64_t in = ((int64_t)u * k + j0) * DD;
-#pragma unroll
-    for (int x = 0; x < V_ROWS * DD / 4 / V_THREADS; ++x) {
-      const int i = x * V_THREADS + threadIdx.x;
-      float *a = &rows[2 * s * V_ROWS][0] + i * 4, *b = a + V_ROWS * DD;
-      if (i / 32 < have) {
-        copy16(a, dS + in + i * 4);
-        copy16(b, H + in + i * 4);
-      } else {
-        *(float4*)a = *(float4*)b = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-    }
-  };
+  const int64_t steps = (int64_t)B * groups;
+  const uint32_t at_w = smem_u32(smem), at_s = at_w + V_OFF_S, at_h = at_w + V_OFF_H;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->full, 512);
+    mbar_init(&bars->done, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
   let_next_start();
-  for (int i = threadIdx.x; i < DD * DD / 4; i += V_THREADS) copy16(sm + i / 32 * W_PITCH + i % 32 * 4, W_V + i * 4);
-  load(blockIdx.x, 0);
-  float acc[8][8] = {};
-  int s = 0;
-  for (int64_t g = blockIdx.x; g < blocks; g += gridDim.x, s ^= 1) {
-    copies_done();
-    __syncthreads();
-    if (g + gridDim.x < blocks) load(g + gridDim.x, s ^ 1);
-    const Rows a = rows + 2 * s * V_ROWS, b = a + V_ROWS;
-    if (warp >= 8) {
-      add_outer<V_ROWS>(b, a, acc);
-      continue;
-    }
-    // rows r0 .. r0 + 3, columns x0 + 16 j
-    const int r0 = 8 * warp + lane / 16 * 4, x0 = lane % 16;
-    const int64_t row0 = g / groups * kp + g % groups * V_ROWS + r0;
-    float v[4][8] = {};
-#pragma unroll 2
-    for (int e = 0; e < DD; e += 4) {
-      float4 x[4];
+
+  if (warp == 16) {
+    if (lane == 0) {
+      const uint32_t id_h = idesc_bf16(128, V_ROWS, false, false), id_w = idesc_bf16(128, 128, true, true);
+      const uint32_t dw = kmajor(at_w), ds = kmajor(at_s);
+      const uint32_t ms = desc_lo(at_s, VS_BYTES / 2), mh = desc_lo(at_h, VS_BYTES / 2);
+      constexpr int pi[6] = {0, 1, 2, 0, 1, 0}, pj[6] = {2, 1, 0, 1, 0, 0};      // parts of the products
+      int n = 0;
+      for (int64_t g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
+        mbar_wait(&bars->full, n & 1, abort, err);
+        tc_fence_after();
+        const uint32_t d = tmem + (n & 1) * V_ROWS, kept = n % kVDrain != 0 ? 1u : 0u;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = *(const float4*)&a[r0 + r][e];
+        for (int o = 0; o < 6; ++o)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float4 w = *(const float4*)(sm + (x0 + 16 * j) * W_PITCH + e);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ss_lo(d, dw + (pi[o] * XT_BYTES >> 4) + kstep(ks),
+                      ds + ((pj[o] * VS_BYTES + (ks >> 2) * (VS_BYTES / 2) + (ks & 3) * 32) >> 4), kHi, id_h, o > 0 || ks > 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[r][j] = fmaf(x[r].x, w.x, fmaf(x[r].y, w.y, fmaf(x[r].z, w.z, fmaf(x[r].w, w.w, v[r][j]))));
+        for (int o = 0; o < 6; ++o)
+#pragma unroll
+          for (int ks = 0; ks < V_ROWS / 16; ++ks)
+            mma_ss_lo(tmem + (o < 5 ? V_TM_DW_LOW : V_TM_DW), mh + (pi[o] * VS_BYTES >> 4) + mnstep(ks),
+                      ms + (pj[o] * VS_BYTES >> 4) + mnstep(ks), kHi, id_w, ks > 0 || (o > 0 && o < 5) ? 1u : kept);
+        mma_commit(&bars->done);
       }
     }
+  } else {
+    const int q = warp % 4, p = warp / 4, c = 32 * q + lane;     // dH's column; rows 16 p .. of a step, 32 p .. of dW_V
+    const uint32_t own = tmem + ((uint32_t)(q * 32) << 16);
+    float4 sv[4], hv[4];
+    auto load = [&](int64_t g) {
+      const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS;
+      const int have = off[u + 1] > off[u] ? k - j0 : 0;
+      const int64_t in = ((int64_t)u * k + j0) * DD;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      float dot = 0.f, dot_hi = 0.f;
+      for (int x = 0; x < 4; ++x) {
+        const int i = x * 512 + threadIdx.x;
+        sv[x] = hv[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i / 32 < have) {
+          sv[x] = *(const float4*)(dS + in + i * 4);
+          hv[x] = *(const float4*)(H + in + i * 4);
+        }
+      }
+    };
+    float acc[32];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = b[r0 + r][x0 + 16 * j];
-        v[r][j] *= inv;
-        const float hi = round_bf16(v[r][j]);
-        dot_hi = fmaf(hi, h, dot_hi);
-        dot = fmaf(hi, h, fmaf(round_bf16(v[r][j] - hi), h, dot));
-      }
-      for (int m = 8; m > 0; m >>= 1) {
-        dot += __shfl_xor_sync(0xffffffffu, dot, m);
-        dot_hi += __shfl_xor_sync(0xffffffffu, dot_hi, m);
-      }
-      if (x0 == 0) {
-        cj[row0 + r] = dot;
-        c2[row0 + r] = kLn2 * dot_hi;
-      }
-      // neighbours exchange columns: an even lane has (x0, x0 + 1) of 16 j, an odd one (x0 - 1, x0) of 16 (j + 1)
-      const bool odd = x0 & 1;
+    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+    auto drain = [&]() {
+      float v[32];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[r][j] : v[r][j + 1], 1);
-        const float first = odd ? got : v[r][j], second = odd ? v[r][j + 1] : got;
-        const int64_t at = (row0 + r) * DD + 16 * (j + odd) + (x0 & ~1);
+      for (int o = 0; o < 2; ++o) {
+        tmem_ld32(own + (o == 0 ? V_TM_DW_LOW : V_TM_DW) + 32 * p, v);
+        wait_ld<32>(v);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[i] += v[i];
+      }
+    };
+    // dH of step g, in TMEM buffer b: hi and lo, c and c2
+    auto write = [&](int64_t g, int b) {
+      const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS + 16 * p;
+      const int have = off[u + 1] > off[u] ? k - j0 : 0;
+      const float* h_at = H + ((int64_t)u * k + j0) * DD + c;
+      const int64_t row0 = (int64_t)u * kp + j0;
+      float v[16], sum[32];
+      tmem_ld16(own + b * V_ROWS + 16 * p, v);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sum[r] = r < have ? h_at[r * DD] : 0.f;
+      wait_ld<16>(v);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] *= inv;
+        const float hi = round_bf16(v[r]), lo = round_bf16(v[r] - hi);
+        sum[16 + r] = fmaf(hi, sum[r], lo * sum[r]);
+        sum[r] *= hi;
+      }
+      // the 32 sums over the warp's columns, one to a lane
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const bool up = lane & o;
+          const float send = up ? sum[i] : sum[i + o], keep = up ? sum[i + o] : sum[i];
+          sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      red[((b * 2 + lane / 16) * 4 + q) * V_ROWS + 16 * p + lane % 16] = sum[0];
+      // neighbours exchange columns: an even lane stores rows 0, 2, .., an odd one 1, 3, ..
+      const bool odd = lane & 1;
+#pragma unroll
+      for (int r = 0; r < 16; r += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[r] : v[r + 1], 1);
         uint32_t hi, lo;
-        split2(first, second, hi, lo);
+        split2(odd ? got : v[r], odd ? v[r + 1] : got, hi, lo);
+        const int64_t at = (row0 + r + odd) * DD + (c & ~1);
         *(uint32_t*)(Hhi + at) = hi;
         *(uint32_t*)(Hlo + at) = lo;
       }
+      asm volatile("bar.sync 1, 512;" ::: "memory");
+      if (threadIdx.x < 2 * V_ROWS) {
+        const int which = threadIdx.x / V_ROWS, r = threadIdx.x % V_ROWS;
+        const float* s = red + (b * 2 + which) * 4 * V_ROWS + r;
+        const float x = (s[0] + s[V_ROWS]) + (s[2 * V_ROWS] + s[3 * V_ROWS]);
+        const int64_t at = (int64_t)u * kp + g % groups * V_ROWS + r;
+        if (which == 0) c2[at] = kLn2 * x;
+        else cj[at] = x;
+      }
+    };
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int i = x * 512 + threadIdx.x;
+      store_parts(at_w, XT_BYTES, i / 32, i % 32, *(const float4*)(W_V + i * 4));
     }
+    load(blockIdx.x);
+    int n = 0;
+    int64_t last = 0;
+    for (int64_t g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
+      if (n > 0) {                                         // a wait that gave up leaves numbers that mean nothing
+        warp_wait(&bars->done, (n - 1) & 1, abort, err);
+        tc_fence_after();
+        if (n % kVDrain == 0) drain();
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int i = x * 512 + threadIdx.x;
+        store_parts(at_s, VS_BYTES, i / 32, i % 32, sv[x]);
+        store_parts(at_h, VS_BYTES, i / 32, i % 32, hv[x]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&bars->full);
+      if (n > 0) write(last, (n - 1) & 1);
+      if (g + gridDim.x < steps) load(g + gridDim.x);
+      last = g;
+    }
+    warp_wait(&bars->done, (n - 1) & 1, abort, err);
+    tc_fence_after();
+    drain();
+    write(last, (n - 1) & 1);
+    float* dst = part_v + (int64_t)blockIdx.x * DD * DD + c * DD + 32 * p;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) *(float4*)(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
   }
-  if (warp >= 8) store_outer(part_v + (int64_t)blockIdx.x * DD * DD, acc, 1.f);
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 16) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
   wait_for_previous();                       // so that what follows this kernel follows U's too
 }
 
@@ -1248,7 +1362,7 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
   if (many)
     SA_TIMED("tw_values_kernel", st,
              launch_after(tw_values_kernel, n_v, V_THREADS, VALUES_SMEM, st, a.off_dev, a.B, a.k, kp, inv, a.W_V, a.dS, a.H,
-                          w.Hhi, w.Hlo, w.c, w.c2, w.part_v));
+                          w.Hhi, w.Hlo, w.c, w.c2, w.part_v, device_status_word()));
   if (a.n_total > 0) {
     CUtensorMap tmX, tmU, tmUlo, tmH, tmHlo, tmU64, tmUlo64, tmH64;
     const int64_t hrows = (int64_t)a.B * kp;

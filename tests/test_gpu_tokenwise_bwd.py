@@ -114,7 +114,7 @@ CASES = [
     ((1,), 1, 1.0), ((2,), 3, 1.0), ((128,), 128, 1.0), ((129,), 129, 2.0), ((256, 257), 64, 1.0),
     ((130, 0, 700, 5, 1), 100, 1.0), ((0, 0, 3), 65, 1.0), ((1, 2000), 200, 4.0), ((5000,), 300, 0.25),
     ((300,) * 7, 384, 1.0), ((37000, 20), 40, 1.0), ((1100, 1024, 1023), 1024, 2.0), ((700, 257), 4096, 1.0),
-    ((2,) * 40, 600, 2.0), ((9, 0, 300, 1) * 10, 130, 1.0), ((17,) * 170, 128, 1.0),
+    ((2,) * 40, 600, 2.0), ((9, 0, 300, 1) * 10, 130, 1.0), ((17,) * 170, 128, 1.0), ((4, 3) * 100, 500, 1.0),
 ]
 
 

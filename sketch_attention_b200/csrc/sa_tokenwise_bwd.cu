@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
 // small ones first (the accumulation truncates at the size of the sum).  64 rows a step:
 //   dH^T = W_V dS^T (lane = column of dH, 64 TMEM columns, two buffers),
 //   dW_V += H^T dS  (K = the rows; the large product and the small ones in accumulators of their own,
-//   which leave TMEM every kVDrain steps and are summed in registers, rounded to nearest).
+//   which leave TMEM every kVDrain steps and are summed in fp32, rounded to nearest).
 // 16 warps split a step's rows into shared memory, then write the step before while the tensor core
 // works (3840 clocks) and the next rows are on their way.  Every CTA has a first step: the grid is
 // no larger than the number of steps.
@@ -1047,7 +1047,7 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
   float* red = (float*)(smem + V_OFF_RED);                       // [buffer][c2, c][quarter of the columns][row]
   volatile int* abort = &bars->abort;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / V_ROWS;
-  const int64_t steps = (int64_t)B * groups;
+  const int steps = B * groups;                                  // B kp < 2^31
   const uint32_t at_w = smem_u32(smem), at_s = at_w + V_OFF_S, at_h = at_w + V_OFF_H;
 
   if (threadIdx.x == 0) {
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
       const uint32_t ms = desc_lo(at_s, VS_BYTES / 2), mh = desc_lo(at_h, VS_BYTES / 2);
       constexpr int pi[6] = {0, 1, 2, 0, 1, 0}, pj[6] = {2, 1, 0, 1, 0, 0};      // parts of the products
       int n = 0;
-      for (int64_t g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
+      for (int g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
         mbar_wait(&bars->full, n & 1, abort, err);
         tc_fence_after();
         const uint32_t d = tmem + (n & 1) * V_ROWS, kept = n % kVDrain != 0 ? 1u : 0u;
@@ -1095,38 +1095,47 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
   } else {
     const int q = warp % 4, p = warp / 4, c = 32 * q + lane;     // dH's column; rows 16 p .. of a step, 32 p .. of dW_V
     const uint32_t own = tmem + ((uint32_t)(q * 32) << 16);
+    struct Step {
+      int u, j0, have;                                           // user, first row, rows of H that count
+    };
     float4 sv[4], hv[4];
-    auto load = [&](int64_t g) {
-      const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS;
-      const int have = off[u + 1] > off[u] ? k - j0 : 0;
-      const int64_t in = ((int64_t)u * k + j0) * DD;
+    auto load = [&](int g) {
+      Step s{g / groups, g % groups * V_ROWS, 0};
+      if (off[s.u + 1] > off[s.u]) s.have = k - s.j0;
+      const int64_t in = ((int64_t)s.u * k + s.j0) * DD;
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int i = x * 512 + threadIdx.x;
         sv[x] = hv[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i / 32 < have) {
+        if (i / 32 < s.have) {
           sv[x] = *(const float4*)(dS + in + i * 4);
           hv[x] = *(const float4*)(H + in + i * 4);
         }
       }
+      return s;
     };
-    float acc[32];
+    // the CTA's part of sum H^T dS lies in memory (L2): a thread's 32 values of it
+    float* part = part_v + (int64_t)blockIdx.x * DD * DD + c * DD + 32 * p;
+    auto drain = [&](bool first) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-    auto drain = [&]() {
-      float v[32];
+      for (int i = 0; i < 32; i += 16) {
+        float lo[16], v[16];
+        tmem_ld16(own + V_TM_DW_LOW + 32 * p + i, lo);
+        tmem_ld16(own + V_TM_DW + 32 * p + i, v);
+        wait_ld<16>(lo);
+        wait_ld<16>(v);
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {
-        tmem_ld32(own + (o == 0 ? V_TM_DW_LOW : V_TM_DW) + 32 * p, v);
-        wait_ld<32>(v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] += v[i];
+        for (int x = 0; x < 16; x += 4) {
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!first) s = *(const float4*)(part + i + x);
+          *(float4*)(part + i + x) = make_float4(s.x + (lo[x] + v[x]), s.y + (lo[x + 1] + v[x + 1]),
+                                                 s.z + (lo[x + 2] + v[x + 2]), s.w + (lo[x + 3] + v[x + 3]));
+        }
       }
     };
-    // dH of step g, in TMEM buffer b: hi and lo, c and c2
-    auto write = [&](int64_t g, int b) {
-      const int u = (int)(g / groups), j0 = (int)(g % groups) * V_ROWS + 16 * p;
-      const int have = off[u + 1] > off[u] ? k - j0 : 0;
+    // dH of a step, in TMEM buffer b: hi and lo, c and c2
+    auto write = [&](const Step& at_step, int b) {
+      const int u = at_step.u, j0 = at_step.j0 + 16 * p, have = at_step.have - 16 * p;
       const float* h_at = H + ((int64_t)u * k + j0) * DD + c;
       const int64_t row0 = (int64_t)u * kp + j0;
       float v[16], sum[32];
@@ -1167,7 +1176,7 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
         const int which = threadIdx.x / V_ROWS, r = threadIdx.x % V_ROWS;
         const float* s = red + (b * 2 + which) * 4 * V_ROWS + r;
         const float x = (s[0] + s[V_ROWS]) + (s[2 * V_ROWS] + s[3 * V_ROWS]);
-        const int64_t at = (int64_t)u * kp + g % groups * V_ROWS + r;
+        const int64_t at = (int64_t)u * kp + at_step.j0 + r;
         if (which == 0) c2[at] = kLn2 * x;
         else cj[at] = x;
       }
@@ -1177,14 +1186,13 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
       const int i = x * 512 + threadIdx.x;
       store_parts(at_w, XT_BYTES, i / 32, i % 32, *(const float4*)(W_V + i * 4));
     }
-    load(blockIdx.x);
+    Step next = load(blockIdx.x), last{};
     int n = 0;
-    int64_t last = 0;
-    for (int64_t g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
+    for (int g = blockIdx.x; g < steps; g += gridDim.x, ++n) {
       if (n > 0) {                                         // a wait that gave up leaves numbers that mean nothing
         warp_wait(&bars->done, (n - 1) & 1, abort, err);
         tc_fence_after();
-        if (n % kVDrain == 0) drain();
+        if (n % kVDrain == 0) drain(n == kVDrain);
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -1195,17 +1203,15 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(&bars->full);
+      const Step now = next;
+      if (g + (int)gridDim.x < steps) next = load(g + gridDim.x);
       if (n > 0) write(last, (n - 1) & 1);
-      if (g + gridDim.x < steps) load(g + gridDim.x);
-      last = g;
+      last = now;
     }
     warp_wait(&bars->done, (n - 1) & 1, abort, err);
     tc_fence_after();
-    drain();
+    drain(n <= kVDrain);
     write(last, (n - 1) & 1);
-    float* dst = part_v + (int64_t)blockIdx.x * DD * DD + c * DD + 32 * p;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) *(float4*)(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
   }
 
   tc_fence_before();

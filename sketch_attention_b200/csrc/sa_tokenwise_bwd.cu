@@ -931,7 +931,7 @@ __device__ __forceinline__ void store_split(__nv_bfloat16* hi, __nv_bfloat16* lo
 }
 
 // CTAs [0, kp / 16): Q = P W_Q and U = Q W_K^T log2(e) / sqrt(d) as hi + lo (zero rows behind k).
-// The others (where the rows are few), 16 prototypes of a user at a time: dH = i dS W_V^T as hi + lo, c = (hi + lo) . H
+// The others (where the rows are few), 16 prototypes of a user each: dH = i dS W_V^T as hi + lo, c = (hi + lo) . H
 // and c2 = ln2 hi . H (zeros for a user without events and behind k), and the CTA's part of sum H^T dS.
 // G - c is small beside G where a softmax has one large weight (x is near H there), so each c is that of
 // the dH which its kernel's G has, hi + lo in E and hi in dX: the rest then costs rest (x - H), not rest x.
@@ -967,40 +967,36 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
       store_split(Uhi, Ulo, (int64_t)(j0 + r) * DD + lane * 4, *(const float4*)&o[r][lane * 4]);
     return;
   }
-  const int part = blockIdx.x - groups, parts = gridDim.x - groups;
-  float dwv[8][8] = {};
+  const int g = blockIdx.x - groups, u = g / groups, j0 = g % groups * RB;
+  const int have = off[u + 1] > off[u] ? k - j0 : 0;
+  const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0;
   load_weight(sm, W_V);
-  for (int64_t g = part; g < (int64_t)B * groups; g += parts) {
-    const int u = (int)(g / groups), j0 = (int)(g % groups) * RB;
-    const int have = off[u + 1] > off[u] ? k - j0 : 0;
-    const int64_t in = ((int64_t)u * k + j0) * DD, row0 = (int64_t)u * kp + j0;
-    __syncthreads();
-    load_block<RB>(a, dS + in, have);
-    load_block<RB>(b, H + in, have);
-    copies_done();
-    __syncthreads();
-    rows_product<RB, true>(a, sm, v);
-    store_column<RB>(o, v, inv);
-    add_outer<RB>(b, a, dwv);
-    __syncthreads();
-    for (int r = warp; r < RB; r += R_THREADS / 32) {
-      const float4 x = *(const float4*)&o[r][lane * 4], hv = *(const float4*)&b[r][lane * 4];
-      const float4 hi = make_float4(round_bf16(x.x), round_bf16(x.y), round_bf16(x.z), round_bf16(x.w));
-      float dot_hi = fmaf(hi.x, hv.x, fmaf(hi.y, hv.y, fmaf(hi.z, hv.z, hi.w * hv.w)));
-      float dot = fmaf(round_bf16(x.x - hi.x), hv.x, fmaf(round_bf16(x.y - hi.y), hv.y,
-                  fmaf(round_bf16(x.z - hi.z), hv.z, fmaf(round_bf16(x.w - hi.w), hv.w, dot_hi))));
-      for (int s = 16; s > 0; s >>= 1) {
-        dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        dot_hi += __shfl_xor_sync(0xffffffffu, dot_hi, s);
-      }
-      if (lane == 0) {
-        cj[row0 + r] = dot;
-        c2[row0 + r] = kLn2 * dot_hi;
-      }
-      store_split(Hhi, Hlo, (row0 + r) * DD + lane * 4, x);
+  load_block<RB>(a, dS + in, have);
+  load_block<RB>(b, H + in, have);
+  copies_done();
+  __syncthreads();
+  rows_product<RB, true>(a, sm, v);
+  store_column<RB>(o, v, inv);
+  float dwv[8][8] = {};
+  add_outer<RB>(b, a, dwv);
+  __syncthreads();
+  for (int r = warp; r < RB; r += R_THREADS / 32) {
+    const float4 x = *(const float4*)&o[r][lane * 4], hv = *(const float4*)&b[r][lane * 4];
+    const float4 hi = make_float4(round_bf16(x.x), round_bf16(x.y), round_bf16(x.z), round_bf16(x.w));
+    float dot_hi = fmaf(hi.x, hv.x, fmaf(hi.y, hv.y, fmaf(hi.z, hv.z, hi.w * hv.w)));
+    float dot = fmaf(round_bf16(x.x - hi.x), hv.x, fmaf(round_bf16(x.y - hi.y), hv.y,
+                fmaf(round_bf16(x.z - hi.z), hv.z, fmaf(round_bf16(x.w - hi.w), hv.w, dot_hi))));
+    for (int s = 16; s > 0; s >>= 1) {
+      dot += __shfl_xor_sync(0xffffffffu, dot, s);
+      dot_hi += __shfl_xor_sync(0xffffffffu, dot_hi, s);
     }
+    if (lane == 0) {
+      cj[row0 + r] = dot;
+      c2[row0 + r] = kLn2 * dot_hi;
+    }
+    store_split(Hhi, Hlo, (row0 + r) * DD + lane * 4, x);
   }
-  store_outer(part_v + (int64_t)part * DD * DD, dwv, 1.f);
+  store_outer(part_v + (int64_t)g * DD * DD, dwv, 1.f);
 }
 
 // The same dH, c, c2 and parts of sum H^T dS where there are many rows (many users), on the tensor
@@ -1311,14 +1307,14 @@ int padded_k(int k) { return (k + TILE - 1) / TILE * TILE; }
 Chunking slice_chunks(int64_t n, int k) {
   return make_chunking(n, std::max(1, device_info().sm_count / (padded_k(k) / TILE)), TILE);
 }
-// whether the rows of dS are many enough for tw_values_kernel: a step for half of the SMs.  A call's
-// time with tw_prepare_kernel alone and with it (us): 1 user x 1024 prototypes 75.9, 86.2; 32 x 128 64.5,
-// 69.4; 5 x 1024 131, 123; 12 x 512 98.5, 84.3; 64 x 1024 354, 319; 512 x 1024 1780, 1593
-bool many_rows(int B, int k) { return (int64_t)B * (padded_k(k) / V_ROWS) >= device_info().sm_count / 2; }
+// whether the rows of dS are many enough for tw_values_kernel: more blocks of rows, U's among them, than
+// SMs.  A call's time with tw_prepare_kernel alone and with it (us): 1 user x 1024 prototypes 80.0, 83.5;
+// 16 x 128 49.3, 53.4; 4 x 512 100.4, 96.1; 4 x 1024 130.6, 118.4; 8 x 512 88.2, 74.5; 64 x 1024 510, 240
+bool many_rows(int B, int k) { return (B + 1LL) * (padded_k(k) / RB) > device_info().sm_count; }
 // CTAs that keep a part of the d x d gradient of W_V each (64 KB written and read again)
 int value_parts(int B, int k) {
   const int64_t rows = (int64_t)B * padded_k(k);
-  return (int)(many_rows(B, k) ? std::min<int64_t>(rows / V_ROWS, device_info().sm_count) : std::min<int64_t>(rows / RB, 128));
+  return (int)(many_rows(B, k) ? std::min<int64_t>(rows / V_ROWS, device_info().sm_count) : rows / RB);
 }
 int weight_parts(int k) { return std::min((k + RW - 1) / RW, 64); }
 Chunking token_chunks(int64_t n) { return make_chunking(n, device_info().sm_count, TILE); }

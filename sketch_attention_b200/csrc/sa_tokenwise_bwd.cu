@@ -837,8 +837,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 // GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
 // carry E back to the weights took two thirds of a small call).  A weight matrix lies in shared
 // memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
-// without bank conflicts, so it serves W and W^T.  A thread has one column and every other four of the
-// 128 terms, a sum per row in registers; the half-warps' halves are added by a shuffle.
+// without bank conflicts, so it serves W and W^T.
 constexpr int R_THREADS = 256, W_PITCH = DD + 4;
 constexpr int RB = 16, RW = 8;                // rows per step of the prepare and the weights kernel
 constexpr uint32_t W_BYTES = DD * W_PITCH * 4, ROW_BYTES = DD * 4;
@@ -866,34 +865,62 @@ __device__ __forceinline__ void load_block(float (*rows)[DD], const float* __res
   }
 }
 
-// out[r] = sum_e rows[r][e] W[e][col], or (kT) W[col][e], col = 16 warp + lane % 16; in both half-warps
+// dst[r][c] = f sum_e rows[r][e] W[e][c], or (kT) f sum_e rows[r][e] W[c][e].  A thread has a 4 x 4 tile and
+// every KS-th four of the 128 terms (8 shared loads of 16 bytes for 64 FMA); its neighbours in the warp
+// have the others, and each of them stores a part of the tile.
 template <int R, bool kT>
-__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float* out) {
-  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, e0 = threadIdx.x % 32 / 16 * 4;
-#pragma unroll
-  for (int r = 0; r < R; ++r) out[r] = 0.f;
+__device__ __forceinline__ void rows_product(const float (*rows)[DD], const float* w, float (*dst)[DD], float f) {
+  constexpr int KS = 32 / R, T = R;             // lanes that share a tile, tiles side by side in a warp
+  static_assert(R == 8 || R == 16, "a warp has 16 or 8 tiles");
+  const int warp = threadIdx.x / 32, h = threadIdx.x % 32 / T, t = threadIdx.x % T;
+  const int r0 = warp / (DD / (4 * T)) * 4, c0 = warp % (DD / (4 * T)) * 4 * T;
+  float v[4][4] = {};
 #pragma unroll 2
-  for (int e = e0; e < DD; e += 8) {
-    float4 v;
-    if (kT) v = *(const float4*)(w + col * W_PITCH + e);
-    else v = make_float4(w[e * W_PITCH + col], w[(e + 1) * W_PITCH + col], w[(e + 2) * W_PITCH + col],
-                         w[(e + 3) * W_PITCH + col]);
+  for (int e = 4 * h; e < DD; e += 4 * KS) {
+    float4 x[4];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float4 x = *(const float4*)&rows[r][e];
-      out[r] = fmaf(x.x, v.x, fmaf(x.y, v.y, fmaf(x.z, v.z, fmaf(x.w, v.w, out[r]))));
+    for (int r = 0; r < 4; ++r) x[r] = *(const float4*)&rows[r0 + r][e];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (kT) {                                 // column c0 + t + T j
+        const float4 y = *(const float4*)(w + (c0 + t + T * j) * W_PITCH + e);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r][j] = fmaf(x[r].x, y.x, fmaf(x[r].y, y.y, fmaf(x[r].z, y.z, fmaf(x[r].w, y.w, v[r][j]))));
+      } else {                                  // term e + j of columns c0 + 4 t ..
+        const float4 y = *(const float4*)(w + (e + j) * W_PITCH + c0 + 4 * t);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float xe = j == 0 ? x[r].x : j == 1 ? x[r].y : j == 2 ? x[r].z : x[r].w;
+          v[r][0] = fmaf(xe, y.x, v[r][0]);
+          v[r][1] = fmaf(xe, y.y, v[r][1]);
+          v[r][2] = fmaf(xe, y.z, v[r][2]);
+          v[r][3] = fmaf(xe, y.w, v[r][3]);
+        }
+      }
     }
   }
+  // rows 2 h', 2 h' + 1 of the tile to the lanes with bit 16 of h', and (KS = 4) one row each
+  float u[2][4], s[4];
+  const bool up = threadIdx.x & 16;
 #pragma unroll
-  for (int r = 0; r < R; ++r) out[r] += __shfl_xor_sync(0xffffffffu, out[r], 16);
-}
-// f times the product's column into rows (each half-warp stores half of them)
-template <int R>
-__device__ __forceinline__ void store_column(float (*rows)[DD], const float* v, float f) {
-  const int col = threadIdx.x / 32 * 16 + threadIdx.x % 16, h = threadIdx.x % 32 / 16;
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-    if (r / (R / 2) == h) rows[r][col] = f * v[r];
+    for (int j = 0; j < 4; ++j)
+      u[r][j] = (up ? v[2 + r][j] : v[r][j]) + __shfl_xor_sync(0xffffffffu, up ? v[r][j] : v[2 + r][j], 16);
+  const int row = r0 + (up ? 2 : 0);
+  if (KS == 4) {
+    const bool up8 = threadIdx.x & 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      s[j] = (up8 ? u[1][j] : u[0][j]) + __shfl_xor_sync(0xffffffffu, up8 ? u[0][j] : u[1][j], 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dst[row + (up8 ? 1 : 0)][kT ? c0 + t + T * j : c0 + 4 * t + j] = f * s[j];
+  } else {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dst[row + r][kT ? c0 + t + T * j : c0 + 4 * t + j] = f * u[r][j];
+  }
 }
 
 // acc[8][8] += sum_r a[r][8 ty ..] b[r][4 tx .. and 64 + 4 tx ..]: a thread's tile of a^T b
@@ -944,7 +971,6 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
   extern __shared__ __align__(16) float sm[];
   float (*a)[DD] = (float (*)[DD])(sm + DD * W_PITCH), (*b)[DD] = a + RB, (*o)[DD] = b + RB;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, groups = kp / RB;
-  float v[RB];
   let_next_start();
   if ((int)blockIdx.x < groups) {
     const int j0 = blockIdx.x * RB;
@@ -952,16 +978,14 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
     load_weight(sm, W_Q);
     copies_done();
     __syncthreads();
-    rows_product<RB, false>(a, sm, v);
-    store_column<RB>(b, v, 1.f);
+    rows_product<RB, false>(a, sm, b, 1.f);
     __syncthreads();
     load_weight(sm, W_K);
     for (int r = warp; r < RB; r += R_THREADS / 32)
       if (j0 + r < k) *(float4*)(Q + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&b[r][lane * 4];
     copies_done();
     __syncthreads();
-    rows_product<RB, true>(b, sm, v);
-    store_column<RB>(o, v, u_scale);
+    rows_product<RB, true>(b, sm, o, u_scale);
     __syncthreads();
     for (int r = warp; r < RB; r += R_THREADS / 32)
       store_split(Uhi, Ulo, (int64_t)(j0 + r) * DD + lane * 4, *(const float4*)&o[r][lane * 4]);
@@ -975,8 +999,7 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
   load_block<RB>(b, H + in, have);
   copies_done();
   __syncthreads();
-  rows_product<RB, true>(a, sm, v);
-  store_column<RB>(o, v, inv);
+  rows_product<RB, true>(a, sm, o, inv);
   float dwv[8][8] = {};
   add_outer<RB>(b, a, dwv);
   __syncthreads();
@@ -1231,7 +1254,7 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
   float *w0 = sm, *w1 = sm + DD * W_PITCH;
   float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  float dwq[8][8] = {}, dwk[8][8] = {}, v[RW];
+  float dwq[8][8] = {}, dwk[8][8] = {};
   let_next_start();
   load_weight(w0, W_K);
   load_weight(w1, W_Q);
@@ -1253,13 +1276,11 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
     }
     copies_done();
     __syncthreads();
-    rows_product<RW, false>(e, w0, v);
-    store_column<RW>(dq, v, rs);
+    rows_product<RW, false>(e, w0, dq, rs);
     add_outer<RW>(e, q, dwk);
     __syncthreads();                         // q and e are no longer read: P and dP replace them
     load_block<RW>(q, P + (int64_t)j0 * DD, k - j0);
-    rows_product<RW, true>(dq, w1, v);
-    store_column<RW>(e, v, 1.f);
+    rows_product<RW, true>(dq, w1, e, 1.f);
     copies_done();
     __syncthreads();
     for (int r = warp; r < RW; r += R_THREADS / 32)

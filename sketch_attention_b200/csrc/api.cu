@@ -403,8 +403,8 @@ sa_status sa_backward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* 
     return fail(SA_ERR_UNSUPPORTED, "sa_backward_tokenwise needs bf16 X and d = 128");
   SA_TRY(check_offsets(offsets_host, B, "offsets_host"));
   const int64_t n = offsets_host[B];
-  if (n >= (1LL << 31) - 256 || (int64_t)B * ((k + 127) / 128 * 128) >= (1LL << 31))
-    return fail(SA_ERR_UNSUPPORTED, "n_total and B * k must be < 2^31 (k rounded up to a multiple of 128)");
+  if (n >= (1LL << 31) - 256 || (B + 1LL) * ((k + 127) / 128 * 128) >= (1LL << 30))
+    return fail(SA_ERR_UNSUPPORTED, "n_total must be < 2^31 and (B + 1) * k < 2^30 (k rounded up to a multiple of 128)");
   if (!(eps >= 0.f)) return fail(SA_ERR_INVALID_ARG, "eps must be >= 0");
   SA_TRY(check_ptr(X, "X", n == 0));
   SA_TRY(check_ptr(offsets_dev, "offsets_dev"));

@@ -114,6 +114,12 @@ __device__ __forceinline__ void load_rows(uint8_t* dst, const CUtensorMap* map, 
   tma_load_2d(dst, map, bar, 0, row);
   tma_load_2d(dst + XT_BYTES / 2, map, bar, 64, row);
 }
+// the same through a map of 64-row boxes (U and dH: the dX kernel takes 64 at a time)
+__device__ __forceinline__ void load_rows64(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int row) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    tma_load_2d(dst + i * (XT_BYTES / 4), map, bar, 64 * (i / 2), row + 64 * (i % 2));
+}
 
 // ============================================================== row statistics
 constexpr int S_NXS = 4;
@@ -144,8 +150,7 @@ struct SParams {
 };
 
 __global__ void __launch_bounds__(S_THREADS, 1)
-    tw_lse_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
-                  const __grid_constant__ CUtensorMap tmUlo, SParams p) {
+    tw_lse_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmR, SParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   SBars* bars = (SBars*)(smem + S_OFF_BAR);
@@ -179,8 +184,8 @@ __global__ void __launch_bounds__(S_THREADS, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     mbar_arrive_expect_tx(&bars->u_full, 2 * XT_BYTES);
-    load_rows(smem + S_OFF_U, &tmU, &bars->u_full, sl * TILE);
-    load_rows(smem + S_OFF_U + XT_BYTES, &tmUlo, &bars->u_full, sl * TILE);
+    load_rows64(smem + S_OFF_U, &tmR, &bars->u_full, sl * TILE);
+    load_rows64(smem + S_OFF_U + XT_BYTES, &tmR, &bars->u_full, p.kp + sl * TILE);
     int issued = 0;
     for_each_tile(p.off, p.B, p.ch, g, [&](int t, int, int, int64_t tb, int64_t, bool, bool) {
       const int s = t % S_NXS;
@@ -344,8 +349,7 @@ struct EParams {
   int* err;
 };
 
-__device__ __forceinline__ void e_cta(const CUtensorMap& tmX, const CUtensorMap& tmU, const CUtensorMap& tmUlo,
-                                      const CUtensorMap& tmH, const CUtensorMap& tmHlo, const EParams& p, int cta) {
+__device__ __forceinline__ void e_cta(const CUtensorMap& tmX, const CUtensorMap& tmR, const EParams& p, int cta) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   EBars* bars = (EBars*)(smem + E_OFF_BAR);
@@ -384,16 +388,16 @@ __device__ __forceinline__ void e_cta(const CUtensorMap& tmX, const CUtensorMap&
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     mbar_arrive_expect_tx(&bars->u_full, 2 * XT_BYTES);
-    load_rows(smem + E_OFF_U, &tmU, &bars->u_full, sl * TILE);
-    load_rows(smem + E_OFF_U + XT_BYTES, &tmUlo, &bars->u_full, sl * TILE);
+    load_rows64(smem + E_OFF_U, &tmR, &bars->u_full, sl * TILE);
+    load_rows64(smem + E_OFF_U + XT_BYTES, &tmR, &bars->u_full, p.kp + sl * TILE);
     int issued_x = 0, issued_h = 0;
     for_each_tile(p.off, p.B, p.ch, g, [&](int t, int piece, int u, int64_t tb, int64_t, bool first, bool) {
       if (first) {
         if (piece > 0 && !mbar_wait(&bars->h_empty, (piece - 1) & 1, abort, p.err)) return false;
         mbar_arrive_expect_tx(&bars->h_full, 2 * XT_BYTES);
-        const int row = (int)((int64_t)u * p.kp + sl * TILE);
-        load_rows(smem + E_OFF_U + 2 * XT_BYTES, &tmH, &bars->h_full, row);
-        load_rows(smem + E_OFF_U + 3 * XT_BYTES, &tmHlo, &bars->h_full, row);
+        const int row = (2 + u) * p.kp + sl * TILE;
+        load_rows64(smem + E_OFF_U + 2 * XT_BYTES, &tmR, &bars->h_full, row);
+        load_rows64(smem + E_OFF_U + 3 * XT_BYTES, &tmR, &bars->h_full, row + p.B * p.kp);
         issued_h = piece + 1;
       }
       const int s = t % E_NXS;
@@ -603,8 +607,7 @@ struct Units {
   }
 };
 
-__device__ __forceinline__ void dx_cta(const CUtensorMap& tmX, const CUtensorMap& tmU, const CUtensorMap& tmUlo,
-                                       const CUtensorMap& tmH, const XParams& p, int cta) {
+__device__ __forceinline__ void dx_cta(const CUtensorMap& tmX, const CUtensorMap& tmR, const XParams& p, int cta) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   XBars* bars = (XBars*)(smem + X_OFF_BAR);
@@ -656,12 +659,13 @@ __device__ __forceinline__ void dx_cta(const CUtensorMap& tmX, const CUtensorMap
         mbar_arrive_expect_tx(&bars->c_full[s], CH_BYTES + 2 * KC * 4);
         uint8_t* cd = smem + X_OFF_CH + s * CH_BYTES;
         const int64_t row = (int64_t)un.u * p.kp + c * KC;
-        tma_load_2d(cd, &tmU, &bars->c_full[s], 0, c * KC);
-        tma_load_2d(cd + 8192, &tmH, &bars->c_full[s], 0, (int)row);
-        tma_load_2d(cd + 16384, &tmU, &bars->c_full[s], 64, c * KC);
-        tma_load_2d(cd + 24576, &tmH, &bars->c_full[s], 64, (int)row);
-        tma_load_2d(cd + 32768, &tmUlo, &bars->c_full[s], 0, c * KC);
-        tma_load_2d(cd + 40960, &tmUlo, &bars->c_full[s], 64, c * KC);
+        const int h_row = 2 * p.kp + (int)row;
+        tma_load_2d(cd, &tmR, &bars->c_full[s], 0, c * KC);
+        tma_load_2d(cd + 8192, &tmR, &bars->c_full[s], 0, h_row);
+        tma_load_2d(cd + 16384, &tmR, &bars->c_full[s], 64, c * KC);
+        tma_load_2d(cd + 24576, &tmR, &bars->c_full[s], 64, h_row);
+        tma_load_2d(cd + 32768, &tmR, &bars->c_full[s], 0, p.kp + c * KC);
+        tma_load_2d(cd + 40960, &tmR, &bars->c_full[s], 64, p.kp + c * KC);
         uint8_t* rd = smem + X_OFF_ROW + s * 2 * KC * 4;
         bulk_load(rd, p.lse2 + row, KC * 4, &bars->c_full[s]);
         bulk_load(rd + KC * 4, p.c2 + row, KC * 4, &bars->c_full[s]);
@@ -823,13 +827,10 @@ static_assert(E_THREADS == X_THREADS, "one launch for both");
 constexpr uint32_t GRADS_SMEM = E_SMEM > X_SMEM ? E_SMEM : X_SMEM;
 
 __global__ void __launch_bounds__(X_THREADS, 1)
-    tw_grads_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmU,
-                    const __grid_constant__ CUtensorMap tmUlo, const __grid_constant__ CUtensorMap tmH,
-                    const __grid_constant__ CUtensorMap tmHlo, const __grid_constant__ CUtensorMap tmU64,
-                    const __grid_constant__ CUtensorMap tmUlo64, const __grid_constant__ CUtensorMap tmH64,
+    tw_grads_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmR,
                     const __grid_constant__ XParams xp, const __grid_constant__ EParams ep, int x_ctas) {
-  if ((int)blockIdx.x < x_ctas) dx_cta(tmX, tmU64, tmUlo64, tmH64, xp, (int)blockIdx.x);
-  else e_cta(tmX, tmU, tmUlo, tmH, tmHlo, ep, (int)blockIdx.x - x_ctas);
+  if ((int)blockIdx.x < x_ctas) dx_cta(tmX, tmR, xp, (int)blockIdx.x);
+  else e_cta(tmX, tmR, ep, (int)blockIdx.x - x_ctas);
 }
 
 // ============================================================== rows of 128 columns
@@ -1353,8 +1354,10 @@ size_t tokenwise_bwd_layout(void* base, int B, int64_t n, int k, int d, Tokenwis
   v.chX = token_chunks(n);
   const size_t G = (size_t)std::max(v.chE.G, 1);
   v.Q = c.take<float>(kd);
-  for (__nv_bfloat16** p : {&v.Uhi, &v.Ulo}) *p = c.take<__nv_bfloat16>(kp * d);
-  for (__nv_bfloat16** p : {&v.Hhi, &v.Hlo}) *p = c.take<__nv_bfloat16>((size_t)B * kp * d);
+  v.Uhi = c.take<__nv_bfloat16>(2 * (1 + (size_t)B) * kp * d);   // one array, one tensor map
+  v.Ulo = v.Uhi + kp * d;
+  v.Hhi = v.Ulo + kp * d;
+  v.Hlo = v.Hhi + (size_t)B * kp * d;
   for (float** p : {&v.c, &v.c2, &v.lse2}) *p = c.take<float>((size_t)B * kp);
   v.stat_user = c.take<float2>((size_t)B * S_PARTS * kp);
   v.stat_slot = c.take<float2>(G * 2 * S_PARTS * kp);
@@ -1387,27 +1390,21 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
              launch_after(tw_values_kernel, n_v, V_THREADS, VALUES_SMEM, st, a.off_dev, a.B, a.k, kp, inv, a.W_V, a.dS, a.H,
                           w.Hhi, w.Hlo, w.c, w.c2, w.part_v, device_status_word()));
   if (a.n_total > 0) {
-    CUtensorMap tmX, tmU, tmUlo, tmH, tmHlo, tmU64, tmUlo64, tmH64;
+    CUtensorMap tmX, tmR;                               // the events; U and dH, hi and lo
     const int64_t hrows = (int64_t)a.B * kp;
     if ((s = map_rows(&tmX, a.X, a.n_total, 128)) != SA_OK) return s;
-    if ((s = map_rows(&tmU, w.Uhi, kp, 128)) != SA_OK) return s;
-    if ((s = map_rows(&tmUlo, w.Ulo, kp, 128)) != SA_OK) return s;
-    if ((s = map_rows(&tmH, w.Hhi, hrows, 128)) != SA_OK) return s;
-    if ((s = map_rows(&tmHlo, w.Hlo, hrows, 128)) != SA_OK) return s;
-    if ((s = map_rows(&tmU64, w.Uhi, kp, 64)) != SA_OK) return s;
-    if ((s = map_rows(&tmUlo64, w.Ulo, kp, 64)) != SA_OK) return s;
-    if ((s = map_rows(&tmH64, w.Hhi, hrows, 64)) != SA_OK) return s;
+    if ((s = map_rows(&tmR, w.Uhi, 2 * (kp + hrows), 64)) != SA_OK) return s;
     SParams sp{a.off_dev, a.B, w.chE, slices, kp, w.stat_user, w.stat_slot, device_status_word()};
     SA_TIMED("tw_lse_kernel", st,
-             launch_after(tw_lse_kernel, w.chE.G * slices, S_THREADS, S_SMEM, st, tmX, tmU, tmUlo, sp));
+             launch_after(tw_lse_kernel, w.chE.G * slices, S_THREADS, S_SMEM, st, tmX, tmR, sp));
     SA_TIMED("tw_lse_combine_kernel", st,
              launch_after(tw_lse_combine_kernel, (unsigned)(hrows / 32), 256, 0, st, a.off_dev, w.chE, a.k, kp, w.stat_user,
                           w.stat_slot, w.lse2));
     XParams xp{a.off_dev, a.B, w.chX, kp, w.lse2, w.c2, (__nv_bfloat16*)a.dX, device_status_word()};
     EParams ep{a.off_dev, a.B, w.chE, slices, a.k, kp, w.lse2, w.c, w.Epart, device_status_word()};
     SA_TIMED("tw_grads_kernel", st,
-             launch_after(tw_grads_kernel, w.chX.G + w.chE.G * slices, X_THREADS, GRADS_SMEM, st, tmX, tmU, tmUlo, tmH,
-                          tmHlo, tmU64, tmUlo64, tmH64, xp, ep, w.chX.G));
+             launch_after(tw_grads_kernel, w.chX.G + w.chE.G * slices, X_THREADS, GRADS_SMEM, st, tmX, tmR, xp, ep,
+                          w.chX.G));
   }
   SA_TIMED("tw_weights_kernel", st,
            launch_after(tw_weights_kernel, n_qk, R_THREADS, WEIGHTS_SMEM, st, a.k, w.chE.G, rs, w.Epart, a.P, w.Q, a.W_Q,

@@ -30,10 +30,12 @@ def _check(lib, ids, acts, dX, vocab, actions, **kw):
     return got
 
 
-# n, vocab, actions, d: one event; sizes around a warp, a list piece (256), a CTA's share; one-row
+# n, vocab, actions, d: one event; sizes around a warp, a list piece (256), a CTA's share, and what one CTA
+# or 64 sort; one-row
 # tables; more and fewer rows than a CTA takes; widths below, at and above a warp's 128 columns
 CASES = [(1, 1, 1, 128), (31, 5, 2, 128), (257, 7, 8, 128), (1000, 1000, 3, 128), (1025, 200_000, 8, 128),
          (4097, 1023, 8, 128), (20_000, 1024, 16, 128), (50_001, 70_000, 8, 128), (3000, 300, 256, 128),
+         (4096, 5000, 8, 128), (65_536, 9000, 4, 64), (65_537, 9000, 4, 64),
          (700, 90, 9, 8), (700, 90, 9, 64), (700, 90, 9, 200), (5000, 3, 2, 264)]
 
 
@@ -157,3 +159,15 @@ def test_the_default_dtype_does_not_matter(lib):
     finally:
         torch.set_default_dtype(torch.float32)
     assert all(got[k].dtype == torch.float32 and torch.equal(got[k], want[k]) for k in want)
+
+
+def test_a_large_vocabulary(lib):
+    """More zeros than the sort takes time for: rows without events are zero, the others their sums."""
+    n, vocab = 150_000, 600_000
+    ids, acts, dX = _inputs(n, vocab, 8, 128, torch.bfloat16, 12)
+    out = {"d_item": torch.full((vocab, 128), 3.0, device="cuda")}
+    got = lib.sa_gather_events_backward(ids, acts, dX, vocab, 8, out=out)
+    ref = torch.zeros(vocab, 128, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dX.double())
+    size = torch.zeros(vocab, 128, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dX.double().abs())
+    count = torch.bincount(ids.long(), minlength=vocab)[:, None]
+    assert bool(((got["d_item"].double() - ref).abs() <= count * 2.0 ** -24 * size).all())

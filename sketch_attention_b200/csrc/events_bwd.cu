@@ -21,10 +21,10 @@
 // the whole item gradient meanwhile (most of it stays zero: a million items, 680K events)
 // with bulk stores out of shared memory, a bounded number in flight: written by ordinary
 // stores of half the warps, the zeros held up the sort's loads until they were all out
-// (40 us for a load, 124 us for both; bulk stores of 16 KB 114, of 2 KB, four at once, 103;
+// (40 us for a load, 124 us for both; bulk stores of 16 KB 114, of 2 KB, a few at once, 103;
 // zeros alone 82, sort alone 38).  The rows with events are written over that.  680K events
 // of a million items (bf16 dX, d = 128), us: sort and zeros 103, windows 53, crossing runs 9: the
-// call 175, 690 MB at 3.9 TB/s.
+// call 174, 690 MB at 4.0 TB/s.
 #include <algorithm>
 #include <mutex>
 

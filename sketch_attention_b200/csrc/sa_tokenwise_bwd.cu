@@ -27,10 +27,10 @@
 //     token.  The tiles alternate: while one tile's A and dZ are computed the
 //     tensor core works on the other's.  A and dZ overwrite the logits in TMEM.
 // 340,000 events x 1024 prototypes (4 users), us: statistics 113 (1.58 PFLOP/s of its 2 products), dX 357
-// and E 394 alone (1.25 and 1.36 PFLOP/s of their 5 and 6), 727 in one launch; rows, weights and sums 54; the
-// call 0.90-0.93 ms back to back.  The clock is at 1.56-1.7 GHz there (power cap).  E's operands come
+// and E 394 alone (1.25 and 1.36 PFLOP/s of their 5 and 6), 727 in one launch; rows, weights and sums 50; the
+// call 0.88-0.93 ms back to back.  The clock is at 1.56-1.7 GHz there (power cap).  E's operands come
 // through shared memory at 128 bytes a clock, 2750 of the 3072 clocks that a tile's products take.
-// Short calls are bound by the chain of six kernels (one user of 300 events: 33 us).
+// Short calls are bound by the chain of six kernels (one user of 300 events: 31 us).
 #include <algorithm>
 #include <mutex>
 
@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 // ============================================================== rows of 128 columns
 // The products with the d x d weights, in fp32 FMA, 16 or 8 rows per CTA step (the framework's tiled fp32
 // GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
-// carry E back to the weights took two thirds of a small call).  A weight matrix lies in shared
+// carry E back to the weights took two thirds of a small call; the four stages of them here take about 6 us each).  A weight matrix lies in shared
 // memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
 // without bank conflicts, so it serves W and W^T.
 constexpr int R_THREADS = 256, W_PITCH = DD + 4;
@@ -1030,7 +1030,8 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
 //   dW_V += H^T dS  (K = the rows; the large product and the small ones in accumulators of their own,
 //   which leave TMEM every kVDrain steps and are summed in fp32, rounded to nearest).
 // 16 warps split a step's rows into shared memory, then write the step before while the tensor core
-// works (3840 clocks) and the next rows are on their way.  Every CTA has a first step: the grid is
+// works (4400 clocks) and the next rows are on their way: 11,000 clocks a step, 0.34 ms for 524,288 rows
+// (2.4 TB/s; the L1 and shared-memory array serves the loads and the MMAs' operands).  Every CTA has a first step: the grid is
 // no larger than the number of steps.
 constexpr int V_ROWS = 64, V_THREADS = 544, kVDrain = 8;
 constexpr uint32_t VS_BYTES = V_ROWS * DD * 2;                   // a part of a step's dS or H

@@ -38,10 +38,10 @@ namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // sorting; one more warp zeroes
 constexpr int kZeroBytes = 2048;             // a bulk store of zeros
-constexpr int64_t kManyZeros = 256 << 20;    // zeros that outlast the sort: two stores at once instead of one (1M items 178 -> 172 us)
+constexpr int64_t kManyZeros = 256 << 20;    // that outlast the sort: two stores at once, not one (1M items 178 -> 172 us)
 constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kAlone = 4096;                 // events that one CTA sorts alone (3000: 27 us a call, 40 with three CTAs)
-constexpr int kFewCtas = 64;                 // sorting CTAs that add up each other's counts themselves (20,000 events: 37 -> 34 us)
+constexpr int kFewCtas = 64;                 // CTAs that add up each other's counts (20,000 events: 37 -> 34 us)
 constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;

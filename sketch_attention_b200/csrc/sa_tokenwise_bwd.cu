@@ -836,8 +836,8 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 // ============================================================== rows of 128 columns
 // The products with the d x d weights, in fp32 FMA, 16 or 8 rows per CTA step (the framework's tiled fp32
 // GEMM takes 12 us for such a product at any k up to 1024; the eleven that fold the prototypes and
-// carry E back to the weights took two thirds of a small call; the four stages of them here take about 6 us each).  A weight matrix lies in shared
-// memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
+// carry E back to the weights took two thirds of a small call; the four stages of them here take about
+// 6 us each).  A weight matrix lies in shared memory as it is in memory, with a pitch of 132 floats: rows and columns of it are then both read
 // without bank conflicts, so it serves W and W^T.
 constexpr int R_THREADS = 256, W_PITCH = DD + 4;
 constexpr int RB = 16, RW = 8;                // rows per step of the prepare and the weights kernel
@@ -886,7 +886,8 @@ __device__ __forceinline__ void rows_product(const float (*rows)[DD], const floa
       if (kT) {                                 // column c0 + t + T j
         const float4 y = *(const float4*)(w + (c0 + t + T * j) * W_PITCH + e);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r][j] = fmaf(x[r].x, y.x, fmaf(x[r].y, y.y, fmaf(x[r].z, y.z, fmaf(x[r].w, y.w, v[r][j]))));
+        for (int r = 0; r < 4; ++r)
+          v[r][j] = fmaf(x[r].x, y.x, fmaf(x[r].y, y.y, fmaf(x[r].z, y.z, fmaf(x[r].w, y.w, v[r][j]))));
       } else {                                  // term e + j of columns c0 + 4 t ..
         const float4 y = *(const float4*)(w + (e + j) * W_PITCH + c0 + 4 * t);
 #pragma unroll
@@ -1031,8 +1032,8 @@ __global__ void __launch_bounds__(R_THREADS, 2) tw_prepare_kernel(
 //   which leave TMEM every kVDrain steps and are summed in fp32, rounded to nearest).
 // 16 warps split a step's rows into shared memory, then write the step before while the tensor core
 // works (4400 clocks) and the next rows are on their way: 11,000 clocks a step, 0.34 ms for 524,288 rows
-// (2.4 TB/s; the L1 and shared-memory array serves the loads and the MMAs' operands).  Every CTA has a first step: the grid is
-// no larger than the number of steps.
+// (2.4 TB/s; the L1 and shared-memory array serves the loads and the MMAs' operands).  Every CTA has a
+// first step: the grid is no larger than the number of steps.
 constexpr int V_ROWS = 64, V_THREADS = 544, kVDrain = 8;
 constexpr uint32_t VS_BYTES = V_ROWS * DD * 2;                   // a part of a step's dS or H
 constexpr uint32_t V_OFF_S = 3 * XT_BYTES, V_OFF_H = V_OFF_S + 3 * VS_BYTES, V_OFF_RED = V_OFF_H + 3 * VS_BYTES;
@@ -1041,7 +1042,7 @@ constexpr uint32_t VALUES_SMEM = V_OFF_BAR + 64 + 1024;
 constexpr uint32_t V_TM_DW = 128, V_TM_DW_LOW = 256;             // dH: columns 0-63 and 64-127
 
 struct VBars {
-  uint64_t full, done;
+  uint64_t full, done, mma_done;
   uint32_t tmem_base;
   int abort;
 };
@@ -1074,6 +1075,7 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
   if (threadIdx.x == 0) {
     mbar_init(&bars->full, 512);
     mbar_init(&bars->done, 1);
+    mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -1112,6 +1114,8 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
                       ms + (pj[o] * VS_BYTES >> 4) + mnstep(ks), kHi, id_w, ks > 0 || (o > 0 && o < 5) ? 1u : kept);
         mma_commit(&bars->done);
       }
+      mma_commit(&bars->mma_done);               // nothing in flight when the CTA ends, whatever gave up
+      mbar_wait_bounded(&bars->mma_done, 0);
     }
   } else {
     const int q = warp % 4, p = warp / 4, c = 32 * q + lane;     // dH's column; rows 16 p .. of a step, 32 p .. of dW_V
@@ -1383,9 +1387,9 @@ sa_status sa_tokenwise_backward_run(const SaBwdArgs& a, const TokenwiseBwdWork& 
   const float rs = 1.f / sqrtf((float)a.d);
   sa_status s;
   SA_TIMED("tw_prepare_kernel", st,
-           (tw_prepare_kernel<<<kp / RB + (many ? 0 : n_v), R_THREADS, PREP_SMEM, st>>>(a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs,
-                                                                   a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi, w.Ulo,
-                                                                   w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
+           (tw_prepare_kernel<<<kp / RB + (many ? 0 : n_v), R_THREADS, PREP_SMEM, st>>>(
+               a.off_dev, a.B, a.k, kp, inv, 1.4426950408889634f * rs, a.P, a.W_Q, a.W_K, a.W_V, a.dS, a.H, w.Q, w.Uhi,
+               w.Ulo, w.Hhi, w.Hlo, w.c, w.c2, w.part_v)));
   if (many)
     SA_TIMED("tw_values_kernel", st,
              launch_after(tw_values_kernel, n_v, V_THREADS, VALUES_SMEM, st, a.off_dev, a.B, a.k, kp, inv, a.W_V, a.dS, a.H,

@@ -232,13 +232,41 @@ def test_two_calls_at_once(lib):
             assert torch.equal(g[name], alone[i % 2][0][name]), name
 
 
-def test_h_of_users_without_events_is_not_read(lib):
-    p, dS = _problem((50, 0, 30), 100)
+@pytest.mark.parametrize("users", [1, 60])
+def test_h_of_users_without_events_is_not_read(lib, users):
+    p, dS = _problem((50, 0, 30) * users, 100)
     clean, H = _run(lib, p, dS)
     H = H.clone()
-    H[1] = float("nan")
-    dS[1] = float("nan")
+    H[1::3] = float("nan")
+    dS[1::3] = float("nan")
     got, _ = _run(lib, p, dS, H=H)
     torch.cuda.synchronize()
     for name in NAMES:
         assert torch.equal(clean[name], got[name]), name
+
+
+@pytest.mark.parametrize("users", [1, 60])
+def test_a_gradient_that_is_not_finite_stays_with_its_user(lib, users):
+    """In dX; the weights' gradients are sums over the users."""
+    p, dS = _problem((50, 20, 30) * users, 100)
+    clean, H = _run(lib, p, dS)
+    dS[1, 7, 3] = float("inf")
+    got, _ = _run(lib, p, dS, H=H)
+    torch.cuda.synchronize()
+    lo, hi = int(p.offsets[1]), int(p.offsets[2])
+    assert not bool(got["dX"][lo:hi].isfinite().any())
+    assert torch.equal(got["dX"][:lo], clean["dX"][:lo]) and torch.equal(got["dX"][hi:], clean["dX"][hi:])
+    for name in ("dP", "dW_Q", "dW_K", "dW_V"):
+        assert not bool(got[name].isfinite().all())
+
+
+def test_the_range_of_gradients(lib):
+    """Powers of two times dS scale every gradient, to the bit where nothing is lost below the range."""
+    for lengths in ((40, 9), (5, 6) * 80):
+        p, dS = _problem(lengths, 128)
+        one, H = _run(lib, p, dS)
+        for scale in (2.0 ** -40, 2.0 ** 30):
+            got, _ = _run(lib, p, dS * scale, H=H)
+            torch.cuda.synchronize()
+            for name in NAMES:
+                assert torch.equal(got[name].double(), one[name].double() * scale), (name, scale)

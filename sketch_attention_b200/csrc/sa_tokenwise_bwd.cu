@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(X_THREADS, 1)
 constexpr int R_THREADS = 256, W_PITCH = DD + 4;
 constexpr int RB = 16, RW = 8;                // rows per step of the prepare and the weights kernel
 constexpr uint32_t W_BYTES = DD * W_PITCH * 4, ROW_BYTES = DD * 4;
-constexpr uint32_t PREP_SMEM = W_BYTES + 3 * RB * ROW_BYTES, WEIGHTS_SMEM = 2 * W_BYTES + 3 * RW * ROW_BYTES;
+constexpr uint32_t PREP_SMEM = W_BYTES + 3 * RB * ROW_BYTES, WEIGHTS_SMEM = 2 * W_BYTES + 4 * RW * ROW_BYTES;
 
 __device__ __forceinline__ void copy16(float* dst, const float* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -1248,6 +1248,21 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
   wait_for_previous();                       // so that what follows this kernel follows U's too
 }
 
+// the sum of four columns of n parts, in order, 16 loads at a time (the last few too: one by one they
+// cost a trip to L2 each)
+__device__ __forceinline__ float4 sum_parts(const float* __restrict__ src, int64_t pitch, int n) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 16) {
+    float4 x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      x[i] = i0 + i < n ? *(const float4*)(src + (i0 + i) * pitch) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) { s.x += x[i].x; s.y += x[i].y; s.z += x[i].z; s.w += x[i].w; }
+  }
+  return s;
+}
+
 // 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
 // the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
 __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
@@ -1258,7 +1273,7 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
                                                                   float* __restrict__ part_qk) {
   extern __shared__ __align__(16) float sm[];
   float *w0 = sm, *w1 = sm + DD * W_PITCH;
-  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW;
+  float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW, (*pr)[DD] = dq + RW;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   float dwq[8][8] = {}, dwk[8][8] = {};
   let_next_start();
@@ -1268,30 +1283,22 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
   for (int j0 = blockIdx.x * RW; j0 < k; j0 += gridDim.x * RW) {
     __syncthreads();
     load_block<RW>(q, Q + (int64_t)j0 * DD, k - j0);
+    load_block<RW>(pr, P + (int64_t)j0 * DD, k - j0);
     for (int r = warp; r < RW; r += R_THREADS / 32) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (j0 + r < k) {
-        const float* src = Epart + (int64_t)(j0 + r) * DD + lane * 4;
-#pragma unroll 8
-        for (int g = 0; g < G; ++g) {
-          const float4 y = *(const float4*)(src + (int64_t)g * k * DD);
-          s.x += y.x; s.y += y.y; s.z += y.z; s.w += y.w;
-        }
-      }
+      if (j0 + r < k) s = sum_parts(Epart + (int64_t)(j0 + r) * DD + lane * 4, (int64_t)k * DD, G);
       *(float4*)&e[r][lane * 4] = s;
     }
     copies_done();
     __syncthreads();
     rows_product<RW, false>(e, w0, dq, rs);
     add_outer<RW>(e, q, dwk);
-    __syncthreads();                         // q and e are no longer read: P and dP replace them
-    load_block<RW>(q, P + (int64_t)j0 * DD, k - j0);
+    __syncthreads();                         // e is no longer read: dP replaces it
     rows_product<RW, true>(dq, w1, e, 1.f);
-    copies_done();
+    add_outer<RW>(pr, dq, dwq);
     __syncthreads();
     for (int r = warp; r < RW; r += R_THREADS / 32)
       if (j0 + r < k) *(float4*)(dP + (int64_t)(j0 + r) * DD + lane * 4) = *(const float4*)&e[r][lane * 4];
-    add_outer<RW>(q, dq, dwq);
   }
   store_outer(part_qk + (int64_t)blockIdx.x * 2 * DD * DD, dwq, 1.f);
   store_outer(part_qk + ((int64_t)blockIdx.x * 2 + 1) * DD * DD, dwk, rs);

@@ -171,3 +171,21 @@ def test_a_large_vocabulary(lib):
     size = torch.zeros(vocab, 128, dtype=torch.float64, device="cuda").index_add_(0, ids.long(), dX.double().abs())
     count = torch.bincount(ids.long(), minlength=vocab)[:, None]
     assert bool(((got["d_item"].double() - ref).abs() <= count * 2.0 ** -24 * size).all())
+
+
+def test_captured_on_an_explicit_stream(lib):
+    x = _inputs(20_000, 900, 4, 128, torch.bfloat16, 13)
+    want = lib.sa_gather_events_backward(*x, 900, 4)
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    temporary = [t.clone() for t in x]
+    with torch.cuda.graph(graph, stream=stream):
+        lib.sa_gather_events_backward(*temporary, 900, 4, stream=stream)   # dropped inside the capture
+        got = lib.sa_gather_events_backward(*x, 900, 4, stream=stream)
+    kept = temporary
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
+    del kept, temporary, graph
+    torch.cuda.synchronize()

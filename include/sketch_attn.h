@@ -217,7 +217,8 @@ size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_
  * without events, as that call writes them) and dS [B,k,d] fp32.
  * dX [n_total, d] bf16 out (must not be X); dP [k,d], dW_Q, dW_K, dW_V [d,d] fp32
  * out (sums over the batch).  bf16 X and d = 128 only (else SA_ERR_UNSUPPORTED),
- * 1 <= k <= 4096.  The weight gradients hold fp32-grade accuracy (within 1e-5
+ * 1 <= k <= 4096, n_total < 2^31, (B + 1) * k < 2^30 (k rounded up to 128s).
+ * The weight gradients hold fp32-grade accuracy (within 1e-5
  * of their norm, 3e-6 to 6e-6 measured); the same inputs give the same bits.  Workspace:
  * sa_backward_tokenwise_workspace bytes, caller owned.  Asynchronous on stream.
  */

@@ -46,6 +46,11 @@ def test_tokenwise_backward_refuses(clib, want, bad):
     assert clib.sa_last_error()
 
 
+def test_tokenwise_backward_refuses_too_many_rows(clib):
+    assert _tokenwise(clib, offsets=(0,) * (1 << 18), k=4096) == UNSUPPORTED
+    assert b"2^30" in clib.sa_last_error()
+
+
 def test_tokenwise_backward_workspace(clib):
     ws = sab.sa_backward_tokenwise_workspace
     assert ws(2, 1000, 200, 128, sab.SA_BF16) >= 2 * 256 * 128 * 2 * 2      # dH as two bf16 parts, k rounded up

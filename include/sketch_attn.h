@@ -218,9 +218,11 @@ size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_
  * dX [n_total, d] bf16 out (must not be X); dP [k,d], dW_Q, dW_K, dW_V [d,d] fp32
  * out (sums over the batch).  bf16 X and d = 128 only (else SA_ERR_UNSUPPORTED),
  * 1 <= k <= 4096, n_total < 2^31, (B + 1) * k < 2^30 (k rounded up to 128s).
- * The weight gradients hold fp32-grade accuracy (within 1e-5
- * of their norm, 3e-6 to 6e-6 measured); the same inputs give the same bits.  Workspace:
- * sa_backward_tokenwise_workspace bytes, caller owned.  Asynchronous on stream.
+ * dW_V is an fp32 product; dP, dW_Q and dW_K hold U, dH and dZ in 16 bits (two bf16
+ * each): 3e-6 to 6e-6 of their norm off for logits of a standard deviation up to
+ * 2, more for larger ones (an error of a logit is a relative error of A: 2e-5 at 8).
+ * The same inputs give the same bits.  Workspace: sa_backward_tokenwise_workspace
+ * bytes, caller owned.  Asynchronous on stream.
  */
 sa_status sa_backward_tokenwise(const void* X, sa_dtype x_dtype, const int64_t* offsets_host,
                                 const int64_t* offsets_dev, int B, int k, int d, const float* P,

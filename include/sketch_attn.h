@@ -596,6 +596,18 @@ sa_status sa_measure_exp2_rate(int mode, double* per_second, sa_stream_t stream)
  */
 sa_status sa_selftest_bounded_wait(long long budget_cycles, sa_stream_t stream);
 
+/*
+ * Self-test of sa_gather_events_backward behind a sort that gave up (no fault): its
+ * sums over a given list, [n] pairs (item id, event number), of any words: a run of
+ * equal ids is written to that row of d_item_table, a pair whose id is outside the
+ * table counts for neither output, an action outside its table for d_item_table
+ * alone, and an event number >= n stands for event 0.  Arguments as there, with
+ * fp32 dX, n >= 1, n_actions <= 16 and both outputs.
+ */
+sa_status sa_selftest_unsorted_events(const uint32_t* list, const float* dX, const uint8_t* action_ids, int64_t n,
+                                      int64_t vocab, int n_actions, int d, float* d_item_table, float* d_action_table,
+                                      void* workspace, size_t ws_bytes, sa_stream_t stream);
+
 /* Number of kernels this library has launched in this process. */
 long long sa_launch_count(void);
 

@@ -37,7 +37,7 @@ EXPORTS = ("sa_version", "sa_last_error", "sa_poll_device_status", "sa_forward_w
            "sa_gather_events_fused_workspace", "sa_measure_exp2_rate", "sa_selftest_bounded_wait",
            "sa_refine_backward_workspace", "sa_refine_backward", "sa_backward_tokenwise_workspace",
            "sa_backward_tokenwise", "sa_gather_events_backward_workspace", "sa_gather_events_backward",
-           "sa_adamw_step")
+           "sa_adamw_step", "sa_selftest_unsorted_events")
 
 
 class SAError(RuntimeError):
@@ -180,6 +180,8 @@ def load(path: Optional[str] = None):
     lib.sa_gather_events_backward_workspace.argtypes = [_i64, _i64, _i, _i]
     lib.sa_gather_events_backward.restype = _i
     lib.sa_gather_events_backward.argtypes = [_vp, _vp, _i64, _vp, _i, _i64, _i, _i, _vp, _vp, _vp, _sz, _vp]
+    lib.sa_selftest_unsorted_events.restype = _i
+    lib.sa_selftest_unsorted_events.argtypes = [_vp, _vp, _vp, _i64, _i64, _i, _i, _vp, _vp, _vp, _sz, _vp]
     lib.sa_adamw_step.restype = _i
     lib.sa_adamw_step.argtypes = [ctypes.POINTER(AdamWTensorC), _i, ctypes.POINTER(AdamWConfigC), _vp]
     lib.sa_launch_count.restype = ctypes.c_longlong
@@ -567,6 +569,27 @@ def selftest_bounded_wait(budget_cycles: int = 2_000_000, stream=None) -> None:
     """Launch a kernel whose only wait cannot complete (bounded to ~budget_cycles);
     the next poll_device_status() raises SAError with SA_ERR_TIMEOUT."""
     _check("sa_selftest_bounded_wait", load().sa_selftest_bounded_wait(budget_cycles, _stream(stream)))
+
+
+def selftest_unsorted_events(pairs: torch.Tensor, dX: torch.Tensor, action_ids: torch.Tensor, vocab: int,
+                             n_actions: int) -> dict:
+    """The sums of sa_gather_events_backward over a given list ``pairs`` [n, 2] (int32 words: item id,
+    event) in place of the sort's; fp32 dX."""
+    lib = load()
+    n, d = dX.shape
+    dev = dX.device
+    _need("dX", dX, torch.float32, (n, d), dev)
+    _need("pairs", pairs, torch.int32, (n, 2), dev)
+    _need("action_ids", action_ids, torch.uint8, (n,), dev)
+    with _at(dev, None):
+        res = {"d_item": torch.empty(vocab, d, dtype=torch.float32, device=dev),
+               "d_action": torch.empty(n_actions, d, dtype=torch.float32, device=dev)}
+        ws = _workspace(None, lib.sa_gather_events_backward_workspace(n, vocab, n_actions, d), dev)
+        st = lib.sa_selftest_unsorted_events(pairs.data_ptr(), dX.data_ptr(), action_ids.data_ptr(), n, vocab, n_actions, d,
+                                             res["d_item"].data_ptr(), res["d_action"].data_ptr(), ws.data_ptr(), ws.nbytes,
+                                             _raw_stream(dev, None))
+        _check("sa_selftest_unsorted_events", st)
+    return res
 
 
 def measure_exp2_rate(mode: int = 1, stream=None) -> float:

@@ -813,6 +813,27 @@ sa_status sa_gather_events_backward(const int32_t* item_ids, const uint8_t* acti
                         (cudaStream_t)stream);
 }
 
+sa_status sa_selftest_unsorted_events(const uint32_t* list, const float* dX, const uint8_t* action_ids, int64_t n,
+                                      int64_t vocab, int n_actions, int d, float* d_item_table, float* d_action_table,
+                                      void* workspace, size_t ws_bytes, sa_stream_t stream) {
+  if (n < 1 || vocab < 1 || n_actions < 1 || n_actions > 16) return fail(SA_ERR_INVALID_ARG, "bad sizes");
+  if (d < 8 || d % 8 != 0) return fail(SA_ERR_UNSUPPORTED, "d must be a positive multiple of 8");
+  if (n >= (1LL << 31) || vocab >= (1LL << 31)) return fail(SA_ERR_UNSUPPORTED, "n and vocab must be < 2^31");
+  SA_TRY(check_ptr(list, "list"));
+  SA_TRY(check_ptr(dX, "dX"));
+  if (!action_ids) return fail(SA_ERR_INVALID_ARG, "action_ids is NULL");
+  SA_TRY(check_ptr(d_item_table, "d_item_table"));
+  SA_TRY(check_ptr(d_action_table, "d_action_table"));
+  const size_t need = events_bwd_layout(nullptr, n, vocab, n_actions, d, nullptr);
+  if (!workspace || ws_bytes < need)
+    return fail(SA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  SA_TRY(check_ptr(workspace, "workspace"));
+  EventsBwdWork w;
+  events_bwd_layout(workspace, n, vocab, n_actions, d, &w);
+  return selftest_unsorted_events(list, dX, action_ids, n, vocab, n_actions, d, d_item_table, d_action_table, w,
+                                  (cudaStream_t)stream);
+}
+
 sa_status sa_adamw_step(const sa_adamw_tensor* tensors, int n_tensors, const sa_adamw_config* config,
                         sa_stream_t stream) {
   if (n_tensors < 0 || (n_tensors > 0 && !tensors)) return fail(SA_ERR_INVALID_ARG, "bad tensor list");

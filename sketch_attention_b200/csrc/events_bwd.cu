@@ -78,8 +78,8 @@ __device__ __forceinline__ void sort_sync() { asm volatile("bar.sync 1, %0;" ::"
 
 // Barrier number `round` (from 1) of the sorting CTAs over a counter that starts at zero.  All of
 // them are resident (cooperative launch); the wait is bounded all the same: past the limit it sets
-// the device error word, and the sort goes on over incomplete counts, every index of which is
-// checked before it is used.
+// the device error word, and the sort goes on over incomplete counts.  The list may then hold any
+// words, so every kernel checks an index that comes from it before it is used.
 __device__ __forceinline__ void grid_sync(unsigned* counter, unsigned ctas, unsigned round, int* err) {
   __threadfence();
   sort_sync();
@@ -389,7 +389,10 @@ __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
         const uint32_t key = next.x, ev = next.y;
         if (b + 32 + lane < p1) next = list_at(b + 32 + lane);   // the next 32 positions, a step ahead
         int act = -1;
-        if (kActions && lane < cnt && key < (uint32_t)vocab) act = acts[ev];
+        if (kActions && lane < cnt && key < (uint32_t)vocab) {
+          const int a = acts[ev];                    // below n_actions, unless the key is not this event's
+          act = a < n_actions ? a : -1;
+        }
         uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
         if (lane == 0) prev = run;
         const unsigned heads = __ballot_sync(0xffffffffu, lane < cnt && key != prev);
@@ -606,18 +609,54 @@ int64_t window_size(int64_t n) {
   return std::max<int64_t>(kMinWin, (n + warps - 1) / warps);
 }
 
+// whether the window kernel adds up the actions too
+bool fused_actions(const float* d_item, const float* d_action, int n_actions) {
+  return d_item && d_action && n_actions <= kFusedActions;
+}
+
+// The windows' sums of the list's rows into d_item, and the action sums with them if fused_actions.
+template <class T>
+sa_status sum_windows(const T* dX, const uint2* list, const uint8_t* acts, int64_t n, int64_t vocab, int n_actions, int d,
+                      float* d_item, float* d_action, const EventsBwdWork& w, cudaStream_t st) {
+  static unsigned long long done = 0;
+  static std::mutex mu;
+  const int64_t win = window_size(n), windows = (n + win - 1) / win;
+  const int ctas = (int)((windows + kSumWarps - 1) / kSumWarps);
+  if (fused_actions(d_item, d_action, n_actions)) {
+    const int smem = kSumWarps * n_actions * 512;
+    set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done, mu);
+    SA_TIMED("window_rows_kernel", st,
+             launch_after(window_rows_kernel<T, true>, ctas, kSumThreads, smem, st, dX, list, acts, n, win, vocab, n_actions,
+                          d, w.first, w.last, w.first_key, w.open_key, d_item, w.action_part));
+  } else {
+    SA_TIMED("window_rows_kernel", st,
+             launch_after(window_rows_kernel<T, false>, ctas, kSumThreads, 0, st, dX, list, acts, n, win, vocab, 0, d,
+                          w.first, w.last, w.first_key, w.open_key, d_item, nullptr));
+  }
+  return SA_OK;
+}
+
+// The runs that cross windows into d_item, and the action sums from their parts.
+sa_status sum_crossing(int64_t n, int n_actions, int d, float* d_item, float* d_action, const EventsBwdWork& w,
+                       cudaStream_t st) {
+  const int64_t win = window_size(n), windows = (n + win - 1) / win;
+  const int parts = fused_actions(d_item, d_action, n_actions) ? (int)((windows + kSumWarps - 1) / kSumWarps) : action_ctas(n);
+  const int ac = d_action ? n_actions : 0;
+  SA_TIMED("crossing_rows_kernel", st,
+           launch_after(crossing_rows_kernel, ac + (d_item ? (int)((windows + kCrossWarps - 1) / kCrossWarps) : 0),
+                        kCrossThreads, 0, st, w.first_key, w.open_key,
+                        windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action));
+  return SA_OK;
+}
+
 template <class T>
 sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, int64_t vocab, int n_actions, int d,
               float* d_item, float* d_action, const EventsBwdWork& w, cudaStream_t st) {
-  static unsigned long long done[3] = {};          // one per kernel
+  static unsigned long long done[2] = {};          // one per kernel
   static std::mutex mu;
   int* err = device_status_word();
-  const bool fused = d_item && d_action && n_actions <= kFusedActions;
-  const int64_t win = window_size(n), windows = (n + win - 1) / win;
-  const int window_ctas = (int)((windows + kSumWarps - 1) / kSumWarps);
-  const int parts = fused ? window_ctas : action_ctas(n);
-  if (d_action && !fused) {
-    const int warps = action_warps(n_actions);
+  if (d_action && !fused_actions(d_item, d_action, n_actions)) {
+    const int warps = action_warps(n_actions), parts = action_ctas(n);
     const int smem = warps * n_actions * 512;
     set_smem_limit_once((const void*)action_rows_kernel<T>, 256 * 512, &done[0], mu);
     SA_TIMED("action_rows_kernel", st,
@@ -642,24 +681,10 @@ sa_status run(const T* dX, const int32_t* ids, const uint8_t* acts, int64_t n, i
                                            dim3(kSortThreads + 32), args, (size_t)smem, st));
     }
     const uint2* list = w.list[(passes - 1) & 1];
-    if (fused) {
-      const int smem = kSumWarps * n_actions * 512;
-      set_smem_limit_once((const void*)window_rows_kernel<T, true>, kSumWarps * kFusedActions * 512, &done[2], mu);
-      SA_TIMED("window_rows_kernel", st,
-               launch_after(window_rows_kernel<T, true>, window_ctas, kSumThreads, smem, st, dX, list, acts, n, win, vocab,
-                            n_actions, d, w.first, w.last, w.first_key, w.open_key, d_item, w.action_part));
-    } else {
-      SA_TIMED("window_rows_kernel", st,
-               launch_after(window_rows_kernel<T, false>, window_ctas, kSumThreads, 0, st, dX, list, acts, n, win, vocab, 0,
-                            d, w.first, w.last, w.first_key, w.open_key, d_item, nullptr));
-    }
+    const sa_status done_windows = sum_windows(dX, list, acts, n, vocab, n_actions, d, d_item, d_action, w, st);
+    if (done_windows != SA_OK) return done_windows;
   }
-  const int ac = d_action ? n_actions : 0;
-  SA_TIMED("crossing_rows_kernel", st,
-           launch_after(crossing_rows_kernel, ac + (d_item ? (int)((windows + kCrossWarps - 1) / kCrossWarps) : 0),
-                        kCrossThreads, 0, st, w.first_key, w.open_key,
-                        windows, d, w.first, w.last, d_item, ac, w.action_part, parts, d_action));
-  return SA_OK;
+  return sum_crossing(n, n_actions, d, d_item, d_action, w, st);
 }
 }  // namespace
 
@@ -695,6 +720,14 @@ sa_status events_bwd_run(const void* dX, sa_dtype dtype, const int32_t* ids, con
   if (dtype == SA_BF16)
     return run((const __nv_bfloat16*)dX, ids, acts, n, vocab, n_actions, d, d_item, d_action, w, st);
   return run((const float*)dX, ids, acts, n, vocab, n_actions, d, d_item, d_action, w, st);
+}
+
+sa_status selftest_unsorted_events(const void* list, const float* dX, const uint8_t* acts, int64_t n, int64_t vocab,
+                                   int n_actions, int d, float* d_item, float* d_action, const EventsBwdWork& w,
+                                   cudaStream_t st) {
+  SA_CUDA(cudaMemsetAsync(d_item, 0, sizeof(float) * vocab * d, st));
+  const sa_status s = sum_windows(dX, (const uint2*)list, acts, n, vocab, n_actions, d, d_item, d_action, w, st);
+  return s != SA_OK ? s : sum_crossing(n, n_actions, d, d_item, d_action, w, st);
 }
 
 }  // namespace sa

@@ -160,6 +160,10 @@ size_t events_bwd_layout(void* base, int64_t n, int64_t vocab, int n_actions, in
 sa_status events_bwd_run(const void* dX, sa_dtype dtype, const int32_t* ids, const uint8_t* acts, int64_t n,
                          int64_t vocab, int n_actions, int d, float* d_item, float* d_action, const EventsBwdWork& w,
                          cudaStream_t st);
+// The sums after the sort over a given list ([n] (item id, event), any words), n >= 1, n_actions <= 16.
+sa_status selftest_unsorted_events(const void* list, const float* dX, const uint8_t* acts, int64_t n, int64_t vocab,
+                                   int n_actions, int d, float* d_item, float* d_action, const EventsBwdWork& w,
+                                   cudaStream_t st);
 
 // AdamW over a list of tensors (adamw.cu).
 sa_status adamw_run(const sa_adamw_tensor* tensors, int n_tensors, const sa_adamw_config& c, cudaStream_t st);

@@ -51,6 +51,9 @@ void prof_end(const char* name, cudaStream_t st);
 // It calls wait_for_previous, which returns when the kernel before it has completed and its writes are
 // visible, before it touches anything that an earlier kernel of the call writes; setup and reads of the
 // caller's inputs may come first.  In an ordinary launch both calls do nothing.
+// Such a kernel (and a device function that it calls) has __restrict__ on the caller's inputs only: it
+// promises that nobody else touches the memory while the kernel runs, and the compiler may then move
+// accesses above wait_for_previous.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class... Params, class... Args>

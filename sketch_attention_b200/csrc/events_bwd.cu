@@ -356,9 +356,9 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;      // no item
 // added to the warp's table of action sums; the CTA's tables go to action_part[CTA][n_actions][d].
 template <class T, bool kActions>
 __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
-    const T* __restrict__ dX, const uint2* __restrict__ list, const uint8_t* __restrict__ acts, int64_t n, int64_t win, int64_t vocab,
-    int n_actions, int d, float* __restrict__ first, float* __restrict__ last, uint32_t* __restrict__ first_key,
-    uint32_t* __restrict__ open_key, float* __restrict__ d_item, float* __restrict__ action_part) {
+    const T* __restrict__ dX, const uint2* list, const uint8_t* __restrict__ acts, int64_t n, int64_t win, int64_t vocab,
+    int n_actions, int d, float* first, float* last, uint32_t* first_key, uint32_t* open_key, float* d_item,
+    float* action_part) {
   extern __shared__ float4 tables[];                 // [kSumWarps][n_actions][32]
   let_next_start();
   wait_for_previous();
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kSumThreads, kWindowCtas) window_rows_kernel(
 }
 
 // sum of rows [b, e) of a [., pitch] array at 4 columns, in order
-__device__ __forceinline__ Cols sum_range(const float* __restrict__ part, int64_t b, int64_t e, int64_t pitch, bool in) {
+__device__ __forceinline__ Cols sum_range(const float* part, int64_t b, int64_t e, int64_t pitch, bool in) {
   Cols acc = zero_cols();
   if (!in) return acc;
   int64_t v = b;
@@ -476,14 +476,9 @@ __device__ __forceinline__ Cols sum_warps(const Cols& mine, Cols (*part)[32]) {
 // CTAs [0, action_ctas): the action sums, one action each, from `parts` CTAs' tables.  The others: a
 // warp per window whose last run goes on: the run's sum is last[w] + first[w + 1] + ... up to the
 // window where it ends.  Runs over 32 windows or more are added by the whole CTA.
-__global__ void __launch_bounds__(kCrossThreads) crossing_rows_kernel(const uint32_t* __restrict__ first_key,
-                                                                    const uint32_t* __restrict__ open_key,
-                                                                    int64_t windows, int d,
-                                                                    const float* __restrict__ first,
-                                                                    const float* __restrict__ last,
-                                                                    float* __restrict__ d_item, int action_ctas,
-                                                                    const float* __restrict__ action_part, int parts,
-                                                                    float* __restrict__ d_action) {
+__global__ void __launch_bounds__(kCrossThreads) crossing_rows_kernel(
+    const uint32_t* first_key, const uint32_t* open_key, int64_t windows, int d, const float* first, const float* last,
+    float* d_item, int action_ctas, const float* action_part, int parts, float* d_action) {
   __shared__ Cols part[kCrossWarps][32];
   __shared__ int64_t long_end[kCrossWarps];
   wait_for_previous();

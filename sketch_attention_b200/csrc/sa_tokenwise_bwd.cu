@@ -290,8 +290,7 @@ __global__ void __launch_bounds__(S_THREADS, 1)
 // a padding prototype (its A = 2^(z - inf) = 0) and for a user without events.  A CTA takes 32
 // prototypes of a user; its 8 warps take the pieces in turn, and their results are added in order.
 __global__ void __launch_bounds__(256) tw_lse_combine_kernel(const int64_t* __restrict__ off, Chunking ch, int k, int kp,
-                                                             const float2* __restrict__ user,
-                                                             const float2* __restrict__ slot, float* __restrict__ lse2) {
+                                                             const float2* user, const float2* slot, float* lse2) {
   __shared__ float2 part[8][32];
   let_next_start();
   wait_for_previous();
@@ -849,7 +848,7 @@ __device__ __forceinline__ void copy16(float* dst, const float* src) {
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // the copies of a weight matrix, and of `have` rows (the others zeros); copies_done, then a barrier
-__device__ __forceinline__ void load_weight(float* w, const float* __restrict__ W) {
+__device__ __forceinline__ void load_weight(float* w, const float* W) {
 #pragma unroll
   for (int x = 0; x < DD * DD / 4 / R_THREADS; ++x) {
     const int i = x * R_THREADS + threadIdx.x;
@@ -857,7 +856,7 @@ __device__ __forceinline__ void load_weight(float* w, const float* __restrict__ 
   }
 }
 template <int R>
-__device__ __forceinline__ void load_block(float (*rows)[DD], const float* __restrict__ src, int have) {
+__device__ __forceinline__ void load_block(float (*rows)[DD], const float* src, int have) {
 #pragma unroll
   for (int x = 0; x < R * DD / 4 / R_THREADS; ++x) {
     const int i = x * R_THREADS + threadIdx.x;
@@ -941,7 +940,7 @@ __device__ __forceinline__ void add_outer(const float (*a)[DD], const float (*b)
       for (int x = 0; x < 8; ++x) acc[i][x] = fmaf(av[i], bv[x], acc[i][x]);
   }
 }
-__device__ __forceinline__ void store_outer(float* __restrict__ part, const float (*acc)[8], float f) {
+__device__ __forceinline__ void store_outer(float* part, const float (*acc)[8], float f) {
   const int ty = threadIdx.x / 16 % 16, tx = threadIdx.x % 16;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -1061,8 +1060,8 @@ __device__ __forceinline__ void store_parts(uint32_t base, uint32_t part_bytes, 
 
 __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
     const int64_t* __restrict__ off, int B, int k, int kp, float inv, const float* __restrict__ W_V,
-    const float* __restrict__ dS, const float* __restrict__ H, __nv_bfloat16* __restrict__ Hhi,
-    __nv_bfloat16* __restrict__ Hlo, float* __restrict__ cj, float* __restrict__ c2, float* __restrict__ part_v, int* err) {
+    const float* __restrict__ dS, const float* __restrict__ H, __nv_bfloat16* Hhi, __nv_bfloat16* Hlo, float* cj, float* c2,
+    float* part_v, int* err) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   VBars* bars = (VBars*)(smem + V_OFF_BAR);
@@ -1250,7 +1249,7 @@ __global__ void __launch_bounds__(V_THREADS, 1) tw_values_kernel(
 
 // the sum of four columns of n parts, in order, 16 loads at a time (the last few too: one by one they
 // cost a trip to L2 each)
-__device__ __forceinline__ float4 sum_parts(const float* __restrict__ src, int64_t pitch, int n) {
+__device__ __forceinline__ float4 sum_parts(const float* src, int64_t pitch, int n) {
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += 16) {
     float4 x[16];
@@ -1265,12 +1264,11 @@ __device__ __forceinline__ float4 sum_parts(const float* __restrict__ src, int64
 
 // 8 prototypes at a time: E = the chunks' parts in order, dQ = E W_K / sqrt(d), dP = dQ W_Q^T, and
 // the CTA's parts of dW_Q = P^T dQ and dW_K = E^T Q / sqrt(d)
-__global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, float rs, const float* __restrict__ Epart,
-                                                                  const float* __restrict__ P,
-                                                                  const float* __restrict__ Q,
+__global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, float rs, const float* Epart,
+                                                                  const float* __restrict__ P, const float* Q,
                                                                   const float* __restrict__ W_Q,
-                                                                  const float* __restrict__ W_K, float* __restrict__ dP,
-                                                                  float* __restrict__ part_qk) {
+                                                                  const float* __restrict__ W_K, float* dP,
+                                                                  float* part_qk) {
   extern __shared__ __align__(16) float sm[];
   float *w0 = sm, *w1 = sm + DD * W_PITCH;
   float (*e)[DD] = (float (*)[DD])(w1 + DD * W_PITCH), (*q)[DD] = e + RW, (*dq)[DD] = q + RW, (*pr)[DD] = dq + RW;
@@ -1306,10 +1304,8 @@ __global__ void __launch_bounds__(R_THREADS, 1) tw_weights_kernel(int k, int G, 
 
 // dW_V = i times the sum of its parts, dW_Q and dW_K the sums of theirs: a CTA per 128 values, its
 // 8 warps over the parts, added in order
-__global__ void __launch_bounds__(R_THREADS) tw_sum_kernel(const float* __restrict__ part_v, int n_v, float inv,
-                                                           const float* __restrict__ part_qk, int n_qk,
-                                                           float* __restrict__ dW_V, float* __restrict__ dW_Q,
-                                                           float* __restrict__ dW_K) {
+__global__ void __launch_bounds__(R_THREADS) tw_sum_kernel(const float* part_v, int n_v, float inv, const float* part_qk,
+                                                           int n_qk, float* dW_V, float* dW_Q, float* dW_K) {
   __shared__ float4 sums[R_THREADS / 32][32];
   wait_for_previous();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;

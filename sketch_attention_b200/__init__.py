@@ -654,35 +654,57 @@ def sa_gather_events_backward(item_ids: torch.Tensor, action_ids: torch.Tensor, 
     return res
 
 
+def _refuse_overlaps(spans: list) -> None:
+    """ValueError where memory that an AdamW step writes belongs to two arrays of its list.  ``spans``:
+    (begin, end, name) of each array, an entry's gradient behind its other arrays."""
+    kept, own = [], set()
+    for begin, end, name in spans:
+        # a gradient that is one of its entry's arrays is read there before it is written, value by value
+        if name != "grad" or (begin, end) not in own:
+            kept.append((begin, end, name))
+        own = set() if name == "grad" else own | {(begin, end)}
+    far = {True: (0, 0, ""), False: (0, 0, "")}     # a gradient or not: the span that ends furthest so far
+    for span in sorted(kept):
+        grad = span[2] == "grad"
+        for other_grad in (True, False):
+            other = far[other_grad]
+            if span[0] < other[1] and not (grad and other_grad):
+                raise ValueError(f"{other[2]} and {span[2]} of the list's tensors share memory: an array that the step "
+                                 "writes may not be in the list twice, not even in part")
+        if span[1] > far[grad][1]:
+            far[grad] = span
+
+
 class AdamWTensors:
     """The tensors of an AdamW step, described once for many steps.  ``tensors``: dicts with
     "param" (fp32), "grad" (fp32 or bf16), "m" and "v" (both fp32, or both float8_e4m3fn with
     "m_scale" and "v_scale", fp32, one value per ADAMW_BLOCK values), all of one size and device;
     optionally "param_bf16" (bf16, receives the rounded parameter) and "weight_decay" (default 0).
     The arrays are held by reference: a step reads and updates them in place.  No array that a step
-    writes may be in the list twice (two blocks of threads would update it at once): ValueError."""
+    writes may be in the list twice or share a part of its memory with another one (two blocks of
+    threads would use it at once): ValueError.  Gradients may be shared."""
 
     def __init__(self, tensors: Sequence[dict]):
         self.tensors = [dict(t) for t in tensors]
         self.c = (AdamWTensorC * max(len(self.tensors), 1))()
         self.device = dev = self.tensors[0]["param"].device if self.tensors else None
         f32, f8 = torch.float32, torch.float8_e4m3fn
+        width = {f32: 4, torch.bfloat16: 2, f8: 1}
+        spans = []                                  # (begin, end, name), an entry's gradient behind its other arrays
 
         def at(t, name, dtype, size):
             x = t[name]
             if not (x.dtype is dtype and x.numel() == size and x.device == dev and x.is_contiguous() and x.is_cuda):
                 _need(name, x if not x.is_contiguous() else x.view(-1), dtype, (size,), dev)
-            return x.data_ptr()
+            begin = x.data_ptr()
+            if size:
+                spans.append((begin, begin + size * width[dtype], name))
+            return begin
 
-        written = [t[name].data_ptr() for t in self.tensors for name in ("param", "m", "v", "m_scale", "v_scale",
-                                                                         "param_bf16")
-                   if t.get(name) is not None and t[name].numel() > 0]
-        if len(set(written)) < len(written):
-            raise ValueError("an array that the step writes is in the list twice")
         for c, t in zip(self.c, self.tensors):
-            n, grad = t["param"].numel(), t["grad"].dtype
+            n = t["param"].numel()
             c.n, c.weight_decay = n, t.get("weight_decay", 0.0)
-            c.param, c.grad, c.grad_dtype = at(t, "param", f32, n), at(t, "grad", grad, n), _dtype_code(t["grad"])
+            c.param = at(t, "param", f32, n)
             if t["m"].dtype is f8:
                 blocks = -(-n // ADAMW_BLOCK)
                 c.state, c.m, c.v = SA_STATE_8BIT, at(t, "m", f8, n), at(t, "v", f8, n)
@@ -691,6 +713,13 @@ class AdamWTensors:
                 c.state, c.m, c.v = SA_STATE_F32, at(t, "m", f32, n), at(t, "v", f32, n)
             if t.get("param_bf16") is not None:
                 c.param_bf16 = at(t, "param_bf16", torch.bfloat16, n)
+            c.grad_dtype = _dtype_code(t["grad"])
+            c.grad = at(t, "grad", t["grad"].dtype, n)
+        order = sorted(spans)
+        for a, b in zip(order, order[1:]):
+            if a[1] > b[0]:                         # two share memory: look whether they may
+                _refuse_overlaps(spans)
+                break
 
 
 def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, *, step: int = 0,

@@ -218,9 +218,19 @@ size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_
  * dX [n_total, d] bf16 out (must not be X); dP [k,d], dW_Q, dW_K, dW_V [d,d] fp32
  * out (sums over the batch).  bf16 X and d = 128 only (else SA_ERR_UNSUPPORTED),
  * 1 <= k <= 4096, n_total < 2^31, (B + 1) * k < 2^30 (k rounded up to 128s).
- * dW_V is an fp32 product; dP, dW_Q and dW_K hold U, dH and dZ in 16 bits (two bf16
- * each): 3e-6 to 6e-6 of their norm off for logits of a standard deviation up to
- * 2, more for larger ones (an error of a logit is a relative error of A: 2e-5 at 8).
+ * Accuracy, as a share of a gradient's norm, for the H that is given: dW_V is an fp32
+ * product (1e-7); dP, dW_Q and dW_K hold U, dH and dZ in 16 bits (two bf16 each): 3e-6
+ * to 6e-6 for logits of a standard deviation up to 2, more for larger ones (an error
+ * of a logit is a relative error of A: 2e-5 at 8); dX is bf16 and takes A, dZ, dH and
+ * U in bf16: 2.7e-3 to 3.4e-3, of which its own rounding is 1.7e-3.
+ * c is formed from H, so an H that is off by e adds -(dH . e) A X to E and i e^T dS to
+ * dW_V.  The H of sa_forward_tokenwise comes from bf16 products, 1e-3 to 5e-3 off;
+ * with it the gradients are off those of the exact forward by
+ *   logits' deviation   1/4     1       2       4       8
+ *   dP, dW_Q, dW_K      5e-5    4e-4    2e-3    5e-3    1e-2
+ *   dX                  2.9e-3  3.1e-3  3.4e-3  4.8e-3  7.8e-3
+ *   dW_V                2e-3    2e-3    2.6e-3  3.2e-3  5e-3
+ * A caller who needs the figures above gives an H of fp32 accuracy.
  * The same inputs give the same bits.  Workspace: sa_backward_tokenwise_workspace
  * bytes, caller owned.  Asynchronous on stream.
  */

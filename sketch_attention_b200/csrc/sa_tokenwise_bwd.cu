@@ -13,7 +13,12 @@
 // a K = 8192 product reads 9e-6 off and drifts with K (85000: 1.6e-5 with signs
 // mixed, 6.6e-5 without), K = 1024 1e-6; so E leaves TMEM every kDrain token
 // tiles (1024 events) and is summed in registers, rounded to nearest.  For dX,
-// Z takes U hi + lo (an error of Z is a relative error of A), the rest bf16.
+// Z takes U hi + lo (an error of Z is a relative error of A), the rest (dH in G and in
+// A^T dH, U in dZ^T U, A, dZ) is bf16, since dX itself is: 2.7e-3 to 3.4e-3 of its norm off
+// where its own rounding is 1.7e-3.  All that for the H that is given: c comes from it, and an
+// H that is off by e adds -(dH . e) A X to E (the forward's H, 1e-3 to 5e-3 off, makes 4e-4 of
+// dP at logits of a standard deviation of 1 and 1e-2 at 8).  c from the recomputed A and G
+// would need G in the statistics' pass, a third product there, and another meaning of H.
 //
 // Three tensor-core passes over the events, each bounded by its products
 // (per 128 events x 128 prototypes, 512 clocks per product at the bf16 rate):

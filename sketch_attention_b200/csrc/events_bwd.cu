@@ -38,10 +38,21 @@ namespace {
 constexpr int kMaxBits = 10;                 // of the id per pass: 1024 bins
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;   // sorting; one more warp zeroes
 constexpr int kZeroBytes = 2048;             // a bulk store of zeros
-constexpr int64_t kManyZeros = 256 << 20;    // that outlast the sort: two stores at once, not one (1M items 178 -> 172 us)
+// Bytes of zeros from which two stores are in flight, not one: faster alone, more in the way of the sort.  A
+// replayed call's us, one and two (bf16 rows, cold L2):
+//   table, GB          0.20       0.27       0.36       0.51       1.0
+//   20,000 events    66,  68    80,  74    98,  84   127, 107   227, 188
+//   200,000          82,  88    94,  97   113, 107   143, 127   244, 207
+//   680,000         133, 141   139, 151   152, 164   184, 178   285, 261
+//   2,000,000       278, 283   285, 295   301, 305   324, 324   413, 418
+// (the border lies higher the more events there are to sort, which the rule does not follow)
+constexpr int64_t kManyZeros = 256 << 20;
 constexpr int kSortPer = 1024;               // events per sorting CTA, at least
 constexpr int kAlone = 4096;                 // events that one CTA sorts alone (3000: 27 us a call, 40 with three CTAs)
-constexpr int kFewCtas = 64;                 // CTAs that add up each other's counts (20,000 events: 37 -> 34 us)
+// CTAs that add up each other's counts, a barrier less a pass, where more have them scanned by a warp per digit.  A
+// replayed call's us, added and scanned: 6 to 12 CTAs 45, 49; 20 47, 51; 38 49, 51; 49 to 69 the same; 76 55,
+// 53-55; 98 57, 55; 118 61, 57; 148 66, 61
+constexpr int kFewCtas = 64;
 constexpr int kHeld = 12;                    // keys (and events) that a sorting lane holds in registers
 constexpr int kMinWin = 32;                  // list positions per window, at least
 constexpr int kSumThreads = 256, kSumWarps = kSumThreads / 32;
@@ -290,7 +301,7 @@ __global__ void __launch_bounds__(kSortThreads + 32, 1) sort_events_kernel(SortA
       if (s.zeros >= kManyZeros) {
         for (int64_t at = first; at < s.zeros; at += step)
           tc::bulk_store_limited<2>(s.zero + at, smem_raw, (uint32_t)min((int64_t)kZeroBytes, s.zeros - at));
-      } else {                                 // slower, and less in the way of the sort (200,000 events 79 -> 76 us)
+      } else {
         for (int64_t at = first; at < s.zeros; at += step)
           tc::bulk_store_limited<1>(s.zero + at, smem_raw, (uint32_t)min((int64_t)kZeroBytes, s.zeros - at));
       }

@@ -685,7 +685,10 @@ class AdamWTensors:
     optionally "param_bf16" (bf16, receives the rounded parameter) and "weight_decay" (default 0).
     The arrays are held by reference: a step reads and updates them in place.  No array that a step
     writes may be in the list twice or share a part of its memory with another one (two blocks of
-    threads would use it at once): ValueError.  Gradients may be shared."""
+    threads would use it at once): ValueError.  Gradients may be shared.  The addresses are taken
+    here, once, and the arrays kept alive: a loop that makes new gradient tensors every step (as
+    zero_grad(set_to_none=True) does) needs a new list every step, 3.5 to 4.7 us of host time a tensor;
+    one that fills the same gradient buffers keeps its list."""
 
     def __init__(self, tensors: Sequence[dict]):
         self.tensors = [dict(t) for t in tensors]
@@ -728,9 +731,11 @@ class AdamWTensors:
 def sa_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, *, step: int = 0,
                   step_dev: Optional[torch.Tensor] = None, lr_dev: Optional[torch.Tensor] = None,
                   grad_scale: Optional[torch.Tensor] = None, stream=None) -> None:
-    """One AdamW step, in place, over an AdamWTensors (or a list of its dicts).  ``step`` counts from
-    1; ``step_dev`` (int64), ``lr_dev`` and ``grad_scale`` (fp32) are optional one-value CUDA tensors
-    read when the step runs (for captured steps, clipping and loss scaling)."""
+    """One AdamW step, in place, over an AdamWTensors, or a list of its dicts, which is checked and
+    described anew in every call (62 tensors: 0.22 ms of host time with fp32 states and 0.29 with 8-bit
+    ones, where an AdamWTensors takes 0.01).  ``step`` counts from 1; ``step_dev`` (int64), ``lr_dev``
+    and ``grad_scale`` (fp32) are optional one-value CUDA tensors read when the step runs (for captured
+    steps, clipping and loss scaling)."""
     lib = load()
     if not isinstance(tensors, AdamWTensors):
         tensors = AdamWTensors(tensors)

@@ -32,10 +32,11 @@
 //     token.  The tiles alternate: while one tile's A and dZ are computed the
 //     tensor core works on the other's.  A and dZ overwrite the logits in TMEM.
 // 340,000 events x 1024 prototypes (4 users), us: statistics 113 (1.58 PFLOP/s of its 2 products), dX 357
-// and E 394 alone (1.25 and 1.36 PFLOP/s of their 5 and 6), 727 in one launch; rows, weights and sums 50; the
-// call 0.88-0.93 ms back to back.  The clock is at 1.56-1.7 GHz there (power cap).  E's operands come
-// through shared memory at 128 bytes a clock, 2750 clocks a tile beside the 6 x 512 of its products.
-// Short calls are bound by the chain of six kernels (one user of 300 events: 31 us).
+// and E 394 alone (1.25 and 1.36 PFLOP/s of their 5 and 6), 727 in one launch; rows, weights and sums 50; a
+// call 1.01 ms (0.88-0.93 in a loop over the same buffers).  The clock is at 1.56-1.7 GHz there (power cap).
+// E's operands come through shared memory at 128 bytes a clock, 2750 clocks a tile beside the 6 x 512 of its
+// products.  Short calls are bound by the chain of six kernels and by the host (one user of 300 events: 37 us,
+// 31 replayed from a graph).
 #include <algorithm>
 #include <mutex>
 

@@ -222,7 +222,9 @@ size_t sa_backward_tokenwise_workspace(int B, int64_t n_total, int k, int d, sa_
  * product (1e-7); dP, dW_Q and dW_K hold U, dH and dZ in 16 bits (two bf16 each): 3e-6
  * to 6e-6 for logits of a standard deviation up to 2, more for larger ones (an error
  * of a logit is a relative error of A: 2e-5 at 8); dX is bf16 and takes A, dZ, dH and
- * U in bf16: 2.7e-3 to 3.4e-3, of which its own rounding is 1.7e-3.
+ * U in bf16: 2.7e-3 to 3.4e-3, of which its own rounding is 1.7e-3 (up to 7e-3 for a
+ * handful of prototypes at a deviation of 8).  Where the terms of a gradient nearly
+ * cancel, as in saturated softmaxes over a few events, its share grows as fp32's does.
  * c is formed from H, so an H that is off by e adds -(dH . e) A X to E and i e^T dS to
  * dW_V.  The H of sa_forward_tokenwise comes from bf16 products, 1e-3 to 5e-3 off;
  * with it the gradients are off those of the exact forward by
